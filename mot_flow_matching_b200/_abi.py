@@ -65,6 +65,20 @@ class MotMoeWeights(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in ("w_router", "w_gate", "w_up", "w_down")]
 
 
+class MotPagedConfig(ctypes.Structure):
+    _fields_ = [("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_size", c_int32),
+                ("kv_dtype", c_int32), ("rms_eps", c_float), ("rope_theta", c_double), ("max_positions", c_int32),
+                ("max_batch", c_int32), ("max_tokens", c_int32), ("max_pages", c_int32)]
+
+
+class MotPagedWeights(ctypes.Structure):
+    _fields_ = [("q_norm", c_void_p), ("k_norm", c_void_p)]
+
+
+class MotPagedPoolC(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("n_pages", c_int32)]
+
+
 # name -> (restype, argtypes); every symbol the headers declare
 SIGNATURES = {
     "mot_attn_query_sizes": (c_int32, [POINTER(MotAttnConfig), c_int32, c_int32, c_int32, POINTER(c_size_t),
@@ -128,6 +142,19 @@ SIGNATURES = {
                                   c_void_p]),
     "mot_moe_get_device_status": (c_int32, [c_void_p, c_void_p]),
     "mot_moe_destroy": (None, [c_void_p]),
+    "mot_paged_create": (c_int32, [POINTER(MotPagedConfig), POINTER(MotPagedWeights), c_void_p, POINTER(c_void_p)]),
+    "mot_paged_batch_create": (c_int32, [c_void_p, POINTER(c_void_p)]),
+    "mot_paged_batch_set": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                      c_void_p]),
+    "mot_paged_query_workspace": (c_int32, [c_void_p, POINTER(c_size_t)]),
+    "mot_paged_append": (c_int32, [c_void_p, c_void_p, c_void_p, POINTER(MotPagedPoolC), c_void_p, c_void_p]),
+    "mot_paged_store": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, POINTER(MotPagedPoolC), c_void_p]),
+    "mot_paged_load": (c_int32, [c_void_p, c_void_p, POINTER(MotPagedPoolC), c_void_p, c_void_p, c_int32, c_void_p]),
+    "mot_paged_attend": (c_int32, [c_void_p, c_void_p, c_void_p, POINTER(MotPagedPoolC), c_void_p, c_void_p, c_void_p,
+                                   c_size_t, c_void_p]),
+    "mot_paged_get_device_status": (c_int32, [c_void_p, c_void_p]),
+    "mot_paged_batch_destroy": (None, [c_void_p]),
+    "mot_paged_destroy": (None, [c_void_p]),
 }
 
 _lib = None

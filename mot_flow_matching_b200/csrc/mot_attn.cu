@@ -1777,3 +1777,6 @@ mot_status mot_dev_saved_layout(const mot_attn_config* cfg, int32_t batch, int32
 
 // ------------------------------------------------------------------ the A3B mixture-of-experts MLP
 #include "mot_moe.cuh"
+
+// paged prefix-KV cache (own ABI, same launch machinery)
+#include "mot_paged.cuh"

@@ -1,0 +1,516 @@
+// mot_paged.cuh -- C ABI of the paged prefix-KV cache (see
+// include/mot_paged.h). Same translation unit as mot_attn.cu.
+//
+// One launch per call:
+//   append   norm + rotation + cache write of the chunk
+//   store    dense cache -> pages
+//   load     pages -> dense cache
+//   attend   attention units cut over the SMs by mot_paged_batch_set
+#pragma once
+
+#include "mot_paged.h"
+#include "paged.cuh"
+
+struct mot_paged {
+  mot_paged_config cfg;
+  int device = 0;
+  int num_sms = 148;
+  int small_ctas = 0;      // grid of the few-rows attention
+  float* gains = nullptr;  // q_norm [128], k_norm [128]
+  float2* rope = nullptr;  // [max_positions, 64]
+  int* status = nullptr;
+};
+
+namespace {
+
+constexpr int kPagedGranule = kSmallWarps * kSmallGroup;  // keys: one 16-key group for every warp of a CTA
+
+// Device tables of a batch object, at fixed offsets (32-bit words) so that a
+// captured call finds them after the batch is set again.
+struct PagedTables {
+  size_t counters, cta_unit0, n_entries, seq_q0, seq_kv, seq_vis, seq_page0, head_words;  // one block, one copy
+  size_t pages, page_seq, tok, units, words;
+  int unit_cap;
+};
+
+PagedTables paged_tables(const mot_paged_config& c, int ctas) {
+  PagedTables t;
+  size_t off = 0;
+  auto take = [&](size_t words) {
+    const size_t o = off;
+    off += round_up(words, 4);
+    return o;
+  };
+  const size_t B = c.max_batch, T = c.max_tokens, G = c.n_q_heads / c.n_kv_heads;
+  t.counters = take(ctas);
+  t.cta_unit0 = take(ctas + 1);
+  t.n_entries = take(1);
+  t.seq_q0 = take(B + 1);
+  t.seq_kv = take(B);
+  t.seq_vis = take(B);
+  t.seq_page0 = take(B + 1);
+  t.head_words = off;
+  t.pages = take(c.max_pages);
+  t.page_seq = take(c.max_pages);
+  t.tok = take(2 * T);
+  const size_t tiles = T * G / kSmallRows + std::min(B, T);
+  t.unit_cap = static_cast<int>(tiles * c.n_kv_heads + ctas);
+  t.units = take(static_cast<size_t>(t.unit_cap) * (sizeof(PagedUnit) / 4));
+  t.words = off;
+  return t;
+}
+
+mot_status check_paged_config(const mot_paged_config* c) {
+  if (!c || c->n_q_heads <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 || c->page_size <= 0 || c->max_positions <= 0 ||
+      c->max_batch <= 0 || c->max_tokens <= 0 || c->max_pages <= 0 || !(c->rms_eps >= 0.f) || !(c->rope_theta > 0.0) ||
+      (c->kv_dtype != MOT_PAGED_BF16 && c->kv_dtype != MOT_PAGED_E4M3))
+    return MOT_ERR_INVALID_ARGUMENT;
+  if (c->head_dim != 128 || c->n_q_heads % c->n_kv_heads != 0 || c->n_q_heads / c->n_kv_heads > 64 ||
+      c->n_q_heads > 1024 ||
+      (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) ||
+      c->max_positions > (1 << 22) || c->max_batch > 4096 || c->max_tokens > (1 << 20) || c->max_pages > (1 << 22) ||
+      static_cast<long long>(c->max_tokens) * c->n_q_heads > (1ll << 26))
+    return MOT_ERR_UNSUPPORTED_SHAPE;
+  return MOT_OK;
+}
+
+void release_paged(mot_paged* h) {
+  if (!h) return;
+  cudaFree(h->gains);
+  cudaFree(h->rope);
+  cudaFree(h->status);
+  delete h;
+}
+
+}  // namespace
+
+struct mot_paged_batch {
+  mot_paged* h = nullptr;
+  PagedTables t;
+  int* dev = nullptr;
+  std::vector<int> host;        // mirror of the device tables
+  std::vector<uint32_t> stamp;  // per page of the pool: set number, for repeated pages
+  std::vector<uint8_t> times;
+  uint32_t set_no = 0;
+  // what the last set described
+  int batch = 0, tokens = 0, entries = 0, n_pages = 0, kv_max = 0, units = 0;
+  bool repeated = false, repeated_written = false;
+};
+
+namespace {
+
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+// Cuts the attention's tiles (sequence, KV head, 8 query rows), each with its
+// own number of keys, over the CTAs: the CTAs take equal shares of the total
+// work in tile order, a tile that straddles a boundary is split there (at a
+// multiple of kPagedGranule keys) and its ranges merged on the device. The
+// share is the smallest that fits; work is counted in granules, a unit's
+// prologue and merge as kUnitCost of them.
+constexpr int kUnitCost = 1, kMinShare = 3;
+
+struct SmallTile {
+  int seq, row0, granules, keys;
+};
+
+int cut_units(const std::vector<SmallTile>& tiles, int heads, int ctas, int share, PagedUnit* units, int unit_cap,
+              int* cta_unit0, int* n_units) {
+  int cta = 0, load = 0, n = 0, slots = 0, counters = 0;
+  if (cta_unit0) cta_unit0[0] = 0;
+  for (const SmallTile& tl : tiles)
+    for (int head = 0; head < heads; ++head) {
+      const int first = n;
+      int at = 0;
+      while (at < tl.granules) {
+        int room = share - load - kUnitCost;
+        if (room < 1 && load > 0) {
+          if (++cta >= ctas) return -1;
+          if (cta_unit0) cta_unit0[cta] = n;
+          load = 0;
+          continue;
+        }
+        room = std::max(room, 1);
+        int take = std::min(room, tl.granules - at);
+        if (units) {
+          if (n >= unit_cap) return -1;
+          units[n] = PagedUnit{tl.seq, head, tl.row0, at * kPagedGranule, std::min(tl.keys, (at + take) * kPagedGranule), 0, 0, 0};
+        }
+        ++n;
+        at += take;
+        load += take + kUnitCost;
+      }
+      const int pieces = n - first;
+      if (units)
+        for (int i = 0; i < pieces; ++i) {
+          units[first + i].slot0 = slots;
+          units[first + i].split = i | (pieces << 16);
+          units[first + i].counter = counters;
+        }
+      if (pieces > 1) {
+        slots += pieces;
+        ++counters;
+      }
+    }
+  if (cta_unit0)
+    for (int i = cta + 1; i <= ctas; ++i) cta_unit0[i] = n;
+  if (n_units) *n_units = n;
+  return cta + 1;
+}
+
+bool paged_device_ok(const mot_paged* h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+// what append, store, load and attend check alike
+mot_status check_paged_call(mot_paged_t h, mot_paged_batch_t bt, const mot_paged_pool* pool) {
+  if (!h || !bt || bt->h != h || !pool || !pool->k || !pool->v || bt->batch <= 0) return MOT_ERR_INVALID_ARGUMENT;
+  const bool e4m3 = h->cfg.kv_dtype == MOT_PAGED_E4M3;
+  if (e4m3 != (pool->k_scale != nullptr) || e4m3 != (pool->v_scale != nullptr) || pool->n_pages < bt->n_pages)
+    return MOT_ERR_INVALID_ARGUMENT;
+  const void* ptrs[] = {pool->k, pool->v, pool->k_scale, pool->v_scale};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return MOT_ERR_ALIGNMENT;
+  if (!paged_device_ok(h)) return MOT_ERR_INVALID_ARGUMENT;
+  return MOT_OK;
+}
+
+PagedPool pool_view(const mot_paged_pool* p) {
+  return PagedPool{static_cast<uint8_t*>(p->k), static_cast<uint8_t*>(p->v), static_cast<uint8_t*>(p->k_scale),
+                   static_cast<uint8_t*>(p->v_scale)};
+}
+
+mot_status paged_copy(mot_paged_t h, mot_paged_batch_t bt, void* k, void* v, int32_t rows, const mot_paged_pool* pool,
+                      bool store, cudaStream_t st) {
+  if (rows < bt->kv_max || (store && bt->repeated)) return MOT_ERR_INVALID_ARGUMENT;
+  if (bt->entries == 0) return MOT_OK;
+  if (!k || !v) return MOT_ERR_INVALID_ARGUMENT;
+  if (!aligned16(k) || !aligned16(v)) return MOT_ERR_ALIGNMENT;
+  const mot_paged_config& c = h->cfg;
+  PagedCopyParams p{};
+  p.dense[0] = static_cast<uint4*>(k);
+  p.dense[1] = static_cast<uint4*>(v);
+  p.pool = pool_view(pool);
+  p.pages = bt->dev + bt->t.pages;
+  p.page_seq = bt->dev + bt->t.page_seq;
+  p.seq_page0 = bt->dev + bt->t.seq_page0;
+  p.seq_kv = bt->dev + bt->t.seq_kv;
+  p.n_entries = bt->dev + bt->t.n_entries;
+  p.rows = rows;
+  p.Hkv = c.n_kv_heads;
+  p.page_shift = log2_of(c.page_size);
+  const long long items = static_cast<long long>(bt->entries) * c.n_kv_heads * 2 * (c.page_size / 16);
+  const int grid = static_cast<int>(std::min<long long>((items + 7) / 8, 8ll * h->num_sms));
+  const bool e4m3 = c.kv_dtype == MOT_PAGED_E4M3;
+  auto kern = e4m3 ? (store ? paged_copy_kernel<true, true> : paged_copy_kernel<true, false>)
+                   : (store ? paged_copy_kernel<false, true> : paged_copy_kernel<false, false>);
+  return launch_pdl(kern, dim3(grid), dim3(256), 0, st, p) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights* w, void* stream, mot_paged_t* out) {
+  if (!out) return MOT_ERR_INVALID_ARGUMENT;
+  *out = nullptr;
+  const mot_status st = check_paged_config(cfg);
+  if (st != MOT_OK) return st;
+  if (!w || !w->q_norm || !w->k_norm) return MOT_ERR_INVALID_ARGUMENT;
+  if (!aligned16(w->q_norm) || !aligned16(w->k_norm)) return MOT_ERR_ALIGNMENT;
+  mot_paged* h = new (std::nothrow) mot_paged();
+  if (!h) return MOT_ERR_CUDA;
+  h->cfg = *cfg;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int per_sm = 0;
+  bool ok = cudaGetDevice(&h->device) == cudaSuccess &&
+            cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) == cudaSuccess &&
+            (cfg->kv_dtype == MOT_PAGED_E4M3
+                 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_attn_small_kernel<true>, kSmallWarps * 32, 0)
+                 : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_attn_small_kernel<false>, kSmallWarps * 32, 0)) ==
+                cudaSuccess &&
+            per_sm > 0 && cudaMalloc(&h->gains, 256 * sizeof(float)) == cudaSuccess &&
+            cudaMalloc(&h->rope, static_cast<size_t>(cfg->max_positions) * 64 * sizeof(float2)) == cudaSuccess &&
+            cudaMalloc(&h->status, sizeof(int)) == cudaSuccess;
+  if (ok) {
+    h->small_ctas = per_sm * h->num_sms;
+    RopeFreq f;
+    for (int j = 0; j < 64; ++j) f.inv[j] = std::pow(cfg->rope_theta, -2.0 * j / 128.0);
+    bf16_to_f32_kernel<<<1, 128, 0, s>>>(static_cast<const __nv_bfloat16*>(w->q_norm), h->gains, 128);
+    bf16_to_f32_kernel<<<1, 128, 0, s>>>(static_cast<const __nv_bfloat16*>(w->k_norm), h->gains + 128, 128);
+    paged_rope_kernel<<<4 * h->num_sms, 256, 0, s>>>(h->rope, cfg->max_positions, f);
+    ok = cudaGetLastError() == cudaSuccess && cudaMemsetAsync(h->status, 0, sizeof(int), s) == cudaSuccess &&
+         cudaStreamSynchronize(s) == cudaSuccess;
+  }
+  if (!ok) {
+    release_paged(h);
+    return MOT_ERR_CUDA;
+  }
+  *out = h;
+  return MOT_OK;
+}
+
+void mot_paged_destroy(mot_paged_t h) { release_paged(h); }
+
+mot_status mot_paged_batch_create(mot_paged_t h, mot_paged_batch_t* out) {
+  if (!out) return MOT_ERR_INVALID_ARGUMENT;
+  *out = nullptr;
+  if (!h || !paged_device_ok(h)) return MOT_ERR_INVALID_ARGUMENT;
+  mot_paged_batch* bt = new (std::nothrow) mot_paged_batch();
+  if (!bt) return MOT_ERR_CUDA;
+  bt->h = h;
+  bt->t = paged_tables(h->cfg, h->small_ctas);
+  bool ok = true;
+  try {
+    bt->host.resize(bt->t.words);
+  } catch (...) {
+    ok = false;
+  }
+  ok = ok && cudaMalloc(&bt->dev, bt->t.words * sizeof(int)) == cudaSuccess;
+  if (!ok) {
+    delete bt;
+    return MOT_ERR_CUDA;
+  }
+  *out = bt;
+  return MOT_OK;
+}
+
+void mot_paged_batch_destroy(mot_paged_batch_t bt) {
+  if (!bt) return;
+  cudaFree(bt->dev);
+  delete bt;
+}
+
+mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_t* q_len, const int32_t* kv_len,
+                               const int32_t* visible, const int32_t* table, int32_t table_stride, int32_t n_pages,
+                               void* stream) {
+  if (!bt || !q_len || !kv_len || batch <= 0 || table_stride < 0 || n_pages <= 0) return MOT_ERR_INVALID_ARGUMENT;
+  mot_paged* h = bt->h;
+  const mot_paged_config& c = h->cfg;
+  if (batch > c.max_batch) return MOT_ERR_UNSUPPORTED_SHAPE;
+  const int shift = log2_of(c.page_size);
+  long long tokens = 0, entries = 0;
+  int kv_max = 0;
+  for (int b = 0; b < batch; ++b) {
+    if (q_len[b] < 0 || kv_len[b] < q_len[b]) return MOT_ERR_INVALID_ARGUMENT;
+    if (visible && (visible[b] < 0 || visible[b] > kv_len[b])) return MOT_ERR_INVALID_ARGUMENT;
+    if (kv_len[b] > c.max_positions) return MOT_ERR_UNSUPPORTED_SHAPE;
+    const int used = (kv_len[b] + c.page_size - 1) >> shift;
+    if (used > table_stride || (used > 0 && !table)) return MOT_ERR_INVALID_ARGUMENT;
+    for (int i = 0; i < used; ++i) {
+      const int id = table[static_cast<size_t>(b) * table_stride + i];
+      if (id < 0 || id >= n_pages) return MOT_ERR_INVALID_ARGUMENT;
+    }
+    tokens += q_len[b];
+    entries += used;
+    kv_max = std::max(kv_max, kv_len[b]);
+  }
+  if (tokens > c.max_tokens || entries > c.max_pages) return MOT_ERR_UNSUPPORTED_SHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (!paged_device_ok(h)) return MOT_ERR_INVALID_ARGUMENT;
+  if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess || capturing != cudaStreamCaptureStatusNone) {
+    cudaGetLastError();
+    return MOT_ERR_INVALID_ARGUMENT;
+  }
+  const PagedTables& t = bt->t;
+  int n_units = 0;
+  try {
+    if (bt->stamp.size() < static_cast<size_t>(n_pages)) {
+      bt->stamp.resize(n_pages, 0u);
+      bt->times.resize(n_pages, 0);
+    }
+    std::vector<SmallTile> tiles;
+    bt->batch = 0;  // nothing is described until the copies below are enqueued
+    ++bt->set_no;
+    int* w = bt->host.data();
+    int q0 = 0, e0 = 0;
+    bool repeated = false;
+    const int group = c.n_q_heads / c.n_kv_heads;
+    for (int b = 0; b < batch; ++b) {
+      const int used = (kv_len[b] + c.page_size - 1) >> shift, past = kv_len[b] - q_len[b];
+      const int* row = table + static_cast<size_t>(b) * table_stride;
+      w[t.seq_q0 + b] = q0;
+      w[t.seq_page0 + b] = e0;
+      w[t.seq_kv + b] = kv_len[b];
+      w[t.seq_vis + b] = visible ? visible[b] : 0;
+      for (int i = 0; i < used; ++i) {
+        const int id = row[i];
+        if (bt->stamp[id] != bt->set_no) {
+          bt->stamp[id] = bt->set_no;
+          bt->times[id] = 1;
+        } else {
+          bt->times[id] = 2;
+          repeated = true;
+        }
+        w[t.pages + e0 + i] = id;
+        w[t.page_seq + e0 + i] = b;
+      }
+      for (int i = 0; i < q_len[b]; ++i) {
+        const int pos = past + i;
+        w[t.tok + 2 * (q0 + i)] = pos;
+        w[t.tok + 2 * (q0 + i) + 1] = row[pos >> shift];
+      }
+      for (int r = 0; r < q_len[b] * group; r += kSmallRows) {
+        const int last = std::min(q_len[b] * group, r + kSmallRows) - 1;
+        const int keys = std::max(w[t.seq_vis + b], past + last / group + 1);
+        tiles.push_back(SmallTile{b, r, (keys + kPagedGranule - 1) / kPagedGranule, keys});
+      }
+      q0 += q_len[b];
+      e0 += used;
+    }
+    w[t.seq_q0 + batch] = q0;
+    w[t.seq_page0 + batch] = e0;
+    w[t.n_entries] = e0;
+    bt->repeated = repeated;
+    bt->repeated_written = false;
+    if (repeated)
+      for (int b = 0; b < batch; ++b)
+        if (q_len[b] > 0)
+          for (int i = (kv_len[b] - q_len[b]) >> shift; i <= (kv_len[b] - 1) >> shift; ++i)
+            bt->repeated_written |= bt->times[table[static_cast<size_t>(b) * table_stride + i]] > 1;
+    // smallest share per CTA that fits
+    long long total = 0;
+    for (const SmallTile& tl : tiles) total += static_cast<long long>(tl.granules + kUnitCost) * c.n_kv_heads;
+    const int ctas = h->small_ctas;
+    long long lo = std::max<long long>(kMinShare, (total + ctas - 1) / ctas), hi = std::max<long long>(lo, total + 1);
+    if (hi > INT_MAX) return MOT_ERR_UNSUPPORTED_SHAPE;
+    while (lo < hi) {
+      const long long mid = lo + (hi - lo) / 2;
+      if (cut_units(tiles, c.n_kv_heads, ctas, static_cast<int>(mid), nullptr, 0, nullptr, nullptr) > 0)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    std::fill(w + t.counters, w + t.counters + ctas, 0);
+    if (cut_units(tiles, c.n_kv_heads, ctas, static_cast<int>(lo), reinterpret_cast<PagedUnit*>(w + t.units), t.unit_cap,
+                  w + t.cta_unit0, &n_units) < 0)
+      return MOT_ERR_UNSUPPORTED_SHAPE;
+  } catch (...) {
+    return MOT_ERR_CUDA;
+  }
+  const size_t pieces[][2] = {{0, t.head_words},
+                              {t.pages, static_cast<size_t>(entries)},
+                              {t.page_seq, static_cast<size_t>(entries)},
+                              {t.tok, static_cast<size_t>(2 * tokens)},
+                              {t.units, static_cast<size_t>(n_units) * (sizeof(PagedUnit) / 4)}};
+  for (const auto& pc : pieces)
+    if (pc[1] > 0 && cudaMemcpyAsync(bt->dev + pc[0], bt->host.data() + pc[0], pc[1] * sizeof(int), cudaMemcpyHostToDevice,
+                                     st) != cudaSuccess)
+      return MOT_ERR_CUDA;
+  bt->batch = batch;
+  bt->tokens = static_cast<int>(tokens);
+  bt->entries = static_cast<int>(entries);
+  bt->n_pages = n_pages;
+  bt->kv_max = kv_max;
+  bt->units = n_units;
+  return MOT_OK;
+}
+
+mot_status mot_paged_query_workspace(mot_paged_batch_t bt, size_t* workspace_bytes) {
+  if (!bt || !workspace_bytes) return MOT_ERR_INVALID_ARGUMENT;
+  // a cut makes at most two ranges, and there are fewer cuts than CTAs
+  *workspace_bytes = static_cast<size_t>(bt->h->small_ctas) * 2 * kSmallSlot * sizeof(float);
+  return MOT_OK;
+}
+
+mot_status mot_paged_append(mot_paged_t h, mot_paged_batch_t bt, const void* qkv, const mot_paged_pool* pool, void* q,
+                            void* stream) {
+  const mot_status cs = check_paged_call(h, bt, pool);
+  if (cs != MOT_OK) return cs;
+  if (bt->repeated_written) return MOT_ERR_INVALID_ARGUMENT;
+  if (bt->tokens == 0) return MOT_OK;
+  if (!qkv || !q) return MOT_ERR_INVALID_ARGUMENT;
+  if (!aligned16(qkv) || !aligned16(q)) return MOT_ERR_ALIGNMENT;
+  const mot_paged_config& c = h->cfg;
+  PagedAppendParams p{};
+  p.qkv = static_cast<const uint4*>(qkv);
+  p.q = static_cast<uint4*>(q);
+  p.pool = pool_view(pool);
+  p.gains = h->gains;
+  p.rope = h->rope;
+  p.tok = reinterpret_cast<const int2*>(bt->dev + bt->t.tok);
+  p.T = bt->tokens;
+  p.Hq = c.n_q_heads;
+  p.Hkv = c.n_kv_heads;
+  p.page_shift = log2_of(c.page_size);
+  p.page_mask = c.page_size - 1;
+  p.eps = c.rms_eps;
+  const int quads = (c.n_q_heads + 2 * c.n_kv_heads + 3) / 4;  // four heads a warp at a time
+  const long long all = static_cast<long long>(p.T) * quads;
+  p.heads_per_lane = static_cast<int>(std::min<long long>(4, std::max<long long>(1, all / (32ll * h->num_sms))));
+  p.strips = (quads + p.heads_per_lane - 1) / p.heads_per_lane;
+  const long long warps = static_cast<long long>(p.T) * p.strips;
+  const int grid = static_cast<int>(std::min<long long>((warps + 7) / 8, 8ll * h->num_sms));
+  auto kern = c.kv_dtype == MOT_PAGED_E4M3 ? paged_append_kernel<true> : paged_append_kernel<false>;
+  return launch_pdl(kern, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? MOT_OK
+                                                                                                          : MOT_ERR_CUDA;
+}
+
+mot_status mot_paged_store(mot_paged_t h, mot_paged_batch_t bt, const void* k, const void* v, int32_t rows,
+                           const mot_paged_pool* pool, void* stream) {
+  const mot_status cs = check_paged_call(h, bt, pool);
+  if (cs != MOT_OK) return cs;
+  return paged_copy(h, bt, const_cast<void*>(k), const_cast<void*>(v), rows, pool, true, static_cast<cudaStream_t>(stream));
+}
+
+mot_status mot_paged_load(mot_paged_t h, mot_paged_batch_t bt, const mot_paged_pool* pool, void* k, void* v,
+                          int32_t rows, void* stream) {
+  const mot_status cs = check_paged_call(h, bt, pool);
+  if (cs != MOT_OK) return cs;
+  return paged_copy(h, bt, k, v, rows, pool, false, static_cast<cudaStream_t>(stream));
+}
+
+mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, const mot_paged_pool* pool, void* o,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const mot_status cs = check_paged_call(h, bt, pool);
+  if (cs != MOT_OK) return cs;
+  if (bt->tokens == 0) return MOT_OK;
+  if (!q || !o || !workspace) return MOT_ERR_INVALID_ARGUMENT;
+  const void* ptrs[] = {q, o, lse, workspace};
+  for (const void* ptr : ptrs)
+    if (ptr && !aligned16(ptr)) return MOT_ERR_ALIGNMENT;
+  size_t need = 0;
+  mot_paged_query_workspace(bt, &need);
+  if (workspace_bytes < need) return MOT_ERR_WORKSPACE_TOO_SMALL;
+  const mot_paged_config& c = h->cfg;
+  PagedAttnParams p{};
+  p.q = static_cast<const uint4*>(q);
+  p.o = static_cast<uint4*>(o);
+  p.lse = lse;
+  p.pool = pool_view(pool);
+  p.seq_q0 = bt->dev + bt->t.seq_q0;
+  p.seq_kv = bt->dev + bt->t.seq_kv;
+  p.seq_vis = bt->dev + bt->t.seq_vis;
+  p.seq_page0 = bt->dev + bt->t.seq_page0;
+  p.pages = bt->dev + bt->t.pages;
+  p.units = reinterpret_cast<const PagedUnit*>(bt->dev + bt->t.units);
+  p.cta_unit0 = bt->dev + bt->t.cta_unit0;
+  p.counters = bt->dev + bt->t.counters;
+  p.part = static_cast<float*>(workspace);
+  p.Hq = c.n_q_heads;
+  p.Hkv = c.n_kv_heads;
+  p.group = c.n_q_heads / c.n_kv_heads;
+  p.page_shift = log2_of(c.page_size);
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
+  p.status = h->status;
+  auto kern = c.kv_dtype == MOT_PAGED_E4M3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>;
+  return launch_pdl(kern, dim3(h->small_ctas), dim3(kSmallWarps * 32), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
+             ? MOT_OK
+             : MOT_ERR_CUDA;
+}
+
+mot_status mot_paged_get_device_status(mot_paged_t h, void* stream) {
+  if (!h) return MOT_ERR_INVALID_ARGUMENT;
+  int v = 0;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOT_ERR_CUDA;
+  if (cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return MOT_ERR_CUDA;
+  if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess) return MOT_ERR_CUDA;
+  return (v & DEV_ERR_TIMEOUT) ? MOT_ERR_TIMEOUT : MOT_OK;
+}
+
+}  // extern "C"

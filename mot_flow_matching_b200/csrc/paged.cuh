@@ -1,0 +1,794 @@
+// paged.cuh -- kernels of the paged prefix-KV cache (include/mot_paged.h):
+// norm + rotation + cache write of a chunk, dense <-> pages, and grouped-query
+// attention of few query rows per sequence over the pages.
+#pragma once
+
+#include <climits>
+
+#include "ptx.cuh"
+
+namespace mot {
+
+// ---------------------------------------------------------------- e4m3 rows
+// value of an e8m0 scale byte: 2^(b - 127), 255 = NaN (2^-127 is an f32 subnormal)
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
+}
+
+// Scale byte of a row with largest magnitude amax: 127 + e, e the smallest
+// integer with amax <= 448 * 2^e, at least -64; 255 when amax is not finite.
+// amax = m 2^x with 1 <= m < 2 and 448 = 1.75 * 2^8, so e = x - 8, or x - 7 when
+// m > 1.75: adding 2^21 - 1 to the bits carries into the exponent exactly then.
+__device__ __forceinline__ uint32_t e8m0_of_amax(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  if (bits >= 0x7f800000u) return 255u;
+  const int e = static_cast<int>((bits + 0x1fffffu) >> 23) - 8;
+  return static_cast<uint32_t>(max(e, 127 - 64));
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// two e4m3 (low half of w) -> f16 pair, exact
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
+  return r;
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4& w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
+  return make_uint4(pack_bf162(f[0], f[1]), pack_bf162(f[2], f[3]), pack_bf162(f[4], f[5]), pack_bf162(f[6], f[7]));
+}
+
+// largest magnitude of 8 values; a NaN among them comes out as NaN
+__device__ __forceinline__ float amax8(const float (&f)[8]) {
+  float m = fmax3_nan(fabsf(f[0]), fabsf(f[1]), fabsf(f[2]));
+  m = fmax3_nan(m, fabsf(f[3]), fabsf(f[4]));
+  m = fmax3_nan(m, fabsf(f[5]), fabsf(f[6]));
+  return fmax3_nan(m, fabsf(f[7]), 0.f);
+}
+
+__device__ __forceinline__ uint2 quant8(const float (&f)[8], uint32_t scale) {
+  if (scale == 255u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  const float inv = __uint_as_float((254u - scale) << 23);  // 2^-e, exact (scale in [63, 247])
+  return make_uint2(pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                    pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+}
+
+// 8 e4m3 values times the row's scale as bf16 (exact)
+__device__ __forceinline__ uint4 dequant8(uint2 w, float scale) {
+  float f[8];
+  const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = e4m3x2_f16x2(u[i >> 1] >> (16 * (i & 1)));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    f[2 * i] = v.x * scale;
+    f[2 * i + 1] = v.y * scale;
+  }
+  return pack_bf16x8(f);
+}
+
+// ---------------------------------------------------------------- RoPE table
+struct RopeFreq {
+  double inv[64];
+};
+
+// (cos, sin) of p theta^(-2j/128), angle in f64, rounded to f32
+__global__ void __launch_bounds__(256) paged_rope_kernel(float2* tab, int positions, const RopeFreq freq) {
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < positions * 64ll; i += gridDim.x * 256ll) {
+    double s, c;
+    sincos(static_cast<double>(i >> 6) * freq.inv[i & 63], &s, &c);
+    tab[i] = make_float2(static_cast<float>(c), static_cast<float>(s));
+  }
+}
+
+// ---------------------------------------------------------------- pool view
+struct PagedPool {
+  uint8_t *k, *v;
+  uint8_t *ks, *vs;  // e8m0 rows, e4m3 pools only
+};
+
+// ---------------------------------------------------------------- append
+struct PagedAppendParams {
+  const uint4* qkv;    // bf16 [T, Hq + 2 Hkv, 128]
+  uint4* q;            // bf16 [T, Hq, 128]
+  PagedPool pool;
+  const float* gains;  // q_norm [128], k_norm [128]
+  const float2* rope;  // [positions, 64]
+  const int2* tok;     // per token: position, page
+  int T, Hq, Hkv, page_mask, page_shift;
+  int strips, heads_per_lane;  // a token's heads are cut into `strips` strips
+  float eps;
+};
+
+// One warp takes one strip of one token's heads, four heads at a time: eight
+// lanes share a head, lane e holding dims 8e..8e+7 and 64 + 8e..+7, so that the
+// rotate-half pair (j, j + 64) sits in one lane, all loads and stores are 16
+// bytes, the norm is three shuffles, and the eight (cos, sin) pairs of a lane
+// serve all its heads.
+template <bool kE4m3>
+__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int H = p.Hq + 2 * p.Hkv;
+  const long long work = static_cast<long long>(p.T) * p.strips;
+  const int lane = lane_id(), sub = lane >> 3, e = lane & 7;
+  for (long long w = blockIdx.x * 8ll + warp_id(); w < work; w += gridDim.x * 8ll) {
+    const int t = static_cast<int>(w / p.strips), strip = static_cast<int>(w % p.strips);
+    const int2 tok = p.tok[t];
+    float2 cs[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float4 r = reinterpret_cast<const float4*>(p.rope + static_cast<long long>(tok.x) * 64 + 8 * e)[i >> 1];
+      cs[i] = make_float2(r.x, r.y);
+      cs[i + 1] = make_float2(r.z, r.w);
+    }
+    const long long page_row = static_cast<long long>(tok.y) * p.Hkv;
+    const int off = tok.x & p.page_mask;
+    const int h_begin = strip * p.heads_per_lane * 4;
+    for (int i = 0; i < p.heads_per_lane; ++i) {
+      const int h = h_begin + 4 * i + sub;
+      const bool live = h < H;
+      uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+      if (live) {
+        const uint4* src = p.qkv + (static_cast<long long>(t) * H + h) * 16;
+        ra = src[e];
+        rb = src[8 + e];
+      }
+      float a[8], b[8];
+      unpack_bf16x8(ra, a);
+      unpack_bf16x8(rb, b);
+      const bool is_v = h >= p.Hq + p.Hkv;
+      float ss = 0.f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) ss = fmaf(a[d], a[d], fmaf(b[d], b[d], ss));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (!is_v) {
+        const float rstd = __frsqrt_rn(ss * (1.0f / 128.0f) + p.eps);
+        const float* gain = p.gains + (h < p.Hq ? 0 : 128) + 8 * e;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          const float x = a[d] * rstd * gain[d], y = b[d] * rstd * gain[64 + d];
+          a[d] = x * cs[d].x - y * cs[d].y;
+          b[d] = y * cs[d].x + x * cs[d].y;
+        }
+      }
+      if (kE4m3) {
+        float m = fmax3_nan(amax8(a), amax8(b), 0.f);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+        if (live && h >= p.Hq) {
+          const int g = h - p.Hq - (is_v ? p.Hkv : 0);
+          const long long row = ((page_row + g) << p.page_shift) + off;
+          uint8_t* dst = (is_v ? p.pool.v : p.pool.k) + row * 128;
+          const uint32_t sc = e8m0_of_amax(m);
+          reinterpret_cast<uint2*>(dst)[e] = quant8(a, sc);
+          reinterpret_cast<uint2*>(dst)[8 + e] = quant8(b, sc);
+          if (e == 0) (is_v ? p.pool.vs : p.pool.ks)[row] = static_cast<uint8_t>(sc);
+        }
+      }
+      if (live && (!kE4m3 || h < p.Hq)) {
+        uint4* dst;
+        if (h < p.Hq) {
+          dst = p.q + (static_cast<long long>(t) * p.Hq + h) * 16;
+        } else {
+          const int g = h - p.Hq - (is_v ? p.Hkv : 0);
+          dst = reinterpret_cast<uint4*>((is_v ? p.pool.v : p.pool.k) + (((page_row + g) << p.page_shift) + off) * 256);
+        }
+        dst[e] = is_v ? ra : pack_bf16x8(a);
+        dst[8 + e] = is_v ? rb : pack_bf16x8(b);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- dense <-> pages
+struct PagedCopyParams {
+  uint4* dense[2];  // k, v: bf16 [B, Hkv, rows, 128]
+  PagedPool pool;
+  const int* pages;      // page of table entry i (all sequences' entries, one after another)
+  const int* page_seq;   // its sequence
+  const int* seq_page0;  // first entry of a sequence
+  const int* seq_kv;
+  const int* n_entries;  // entries of the batch as it is set now
+  int rows, Hkv, page_shift;
+};
+
+// A warp takes 16 rows of one (entry, head, k or v): a page is contiguous per
+// head, and so is the dense cache, so both sides are straight runs of 16 rows;
+// all of a lane's loads are issued before the first is used. Eight lanes share
+// a row, 16 values each (32 bytes of bf16, 16 of e4m3), four rows at a time.
+// kStore: dense -> pages; otherwise pages -> dense.
+template <bool kE4m3, bool kStore>
+__global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__ PagedCopyParams p) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = lane_id(), sub = lane >> 3, e = lane & 7;
+  const int runs = 1 << (p.page_shift - 4);
+  const long long items = static_cast<long long>(*p.n_entries) * p.Hkv * 2 * runs;
+  for (long long w = blockIdx.x * 8ll + warp_id(); w < items; w += gridDim.x * 8ll) {
+    const int run = static_cast<int>(w & (runs - 1));
+    long long r = w >> (p.page_shift - 4);
+    const int kv = static_cast<int>(r & 1);
+    r >>= 1;
+    const int head = static_cast<int>(r % p.Hkv), entry = static_cast<int>(r / p.Hkv);
+    const int seq = p.page_seq[entry];
+    const int j0 = ((entry - p.seq_page0[seq]) << p.page_shift) + run * 16;
+    const int live = p.seq_kv[seq] - j0;  // rows of this run that the sequence has
+    if (live <= 0) continue;
+    const long long prow = ((static_cast<long long>(p.pages[entry]) * p.Hkv + head) << p.page_shift) + run * 16;
+    const long long drow = (static_cast<long long>(seq) * p.Hkv + head) * p.rows + j0;
+    uint4* dense = p.dense[kv] + drow * 16;
+    uint8_t* page = (kv ? p.pool.v : p.pool.k) + prow * (kE4m3 ? 128 : 256);
+    uint8_t* scale = kE4m3 ? (kv ? p.pool.vs : p.pool.ks) + prow : nullptr;
+    if (!kE4m3) {
+      uint4* pg = reinterpret_cast<uint4*>(page);
+      const uint4* src = kStore ? dense : pg;
+      uint4* dst = kStore ? pg : dense;
+      uint4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (2 * i + (lane >> 4) < live) x[i] = src[i * 32 + lane];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (2 * i + (lane >> 4) < live) dst[i * 32 + lane] = x[i];
+    } else if (kStore) {
+      uint4 x[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + sub;
+        x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+        if (row < live) {
+          x[i][0] = dense[row * 16 + 2 * e];
+          x[i][1] = dense[row * 16 + 2 * e + 1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + sub;
+        float a[8], b[8];
+        unpack_bf16x8(x[i][0], a);
+        unpack_bf16x8(x[i][1], b);
+        float m = fmax3_nan(amax8(a), amax8(b), 0.f);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+        const uint32_t sc = e8m0_of_amax(m);
+        const uint2 lo = quant8(a, sc), hi = quant8(b, sc);
+        if (row < live) {
+          reinterpret_cast<uint4*>(page + row * 128)[e] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          if (e == 0) scale[row] = static_cast<uint8_t>(sc);
+        }
+      }
+    } else {
+      uint4 x[4];
+      uint32_t sc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + sub;
+        if (row < live) {
+          x[i] = reinterpret_cast<const uint4*>(page + row * 128)[e];
+          sc[i] = scale[row];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + sub;
+        if (row < live) {
+          const float s = e8m0_value(sc[i]);
+          dense[row * 16 + 2 * e] = dequant8(make_uint2(x[i].x, x[i].y), s);
+          dense[row * 16 + 2 * e + 1] = dequant8(make_uint2(x[i].z, x[i].w), s);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- attention, few rows
+// A unit is a tile of query rows of one (sequence, KV head) and a range of its
+// keys. Query rows are (token, head of the group) pairs, head fastest, so the
+// tile reads the KV head's keys once for the whole group.
+struct PagedUnit {
+  int seq, head, row0, key0, key1;
+  int slot0;   // first partial slot of the tile (nsplit > 1)
+  int split;   // this range's number | nsplit << 16
+  int counter; // arrival counter of the tile
+};
+
+struct PagedAttnParams {
+  const uint4* q;  // bf16 [T, Hq, 128]
+  uint4* o;        // bf16 [T, Hq, 128]
+  float* lse;      // [T, Hq] or null
+  PagedPool pool;
+  const int *seq_q0, *seq_kv, *seq_vis, *seq_page0, *pages;
+  const PagedUnit* units;
+  const int* cta_unit0;  // units of CTA i: [cta_unit0[i], cta_unit0[i + 1])
+  int* counters;
+  float* part;  // slots: [rows][128] f32 sums, then [rows] (m, l)
+  int Hq, Hkv, group, page_shift;
+  float scale_log2;  // log2(e) / sqrt(128)
+  int* status;
+};
+
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
+
+// natural-log sum of exponentials from the base-2 running max and sum
+__device__ __forceinline__ float lse_of(float m2, float l) { return (m2 + log2f(l)) * 0.69314718055994531f; }
+
+template <bool kBf16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  if (kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+constexpr int kSmallRows = 8;     // query rows of a unit
+constexpr int kSmallWarps = 8;
+constexpr int kSmallGroup = 16;   // keys a warp takes at a time
+constexpr int kSmallSlot = kSmallRows * 128 + kSmallRows * 2;  // floats of a partial
+
+// One 16-key group's registers: keys as the A operand of S^T = K Q^T (lane
+// (g, c) = (lane / 4, lane % 4) holds keys g and g + 8), values as the A operand
+// of O^T += V^T P^T (keys 2c, 2c+1, 2c+8, 2c+9). The dims each register pair
+// stands for are permuted so that every lane loads whole 16-byte pieces and a
+// warp's load covers whole sectors; the same permutation is applied to Q, and the
+// permuted rows of O^T are consecutive dims of a lane.
+template <bool kE4m3>
+struct KvGroup;
+
+template <>
+struct KvGroup<false> {
+  uint4 k[2][4];
+  uint4 v[4][2];
+  __device__ __forceinline__ void load_k(const PagedPool& p, long long row, int g, int c) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        k[r][i] = __ldg(reinterpret_cast<const uint4*>(p.k) + (row + g + 8 * r) * 16 + 4 * i + c);
+  }
+  __device__ __forceinline__ void load_v(const PagedPool& p, long long row, int g, int c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        v[s][j] = __ldg(reinterpret_cast<const uint4*>(p.v) + (row + 2 * c + (s & 1) + 8 * (s >> 1)) * 16 + 8 * j + g);
+  }
+};
+
+template <>
+struct KvGroup<true> {
+  uint4 k[2][2];
+  uint4 v[4];
+  uint32_t ks[2], vs[2];  // scale bytes of keys g, g + 8
+  __device__ __forceinline__ void load_k(const PagedPool& p, long long row, int g, int c) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        k[r][i] = __ldg(reinterpret_cast<const uint4*>(p.k) + (row + g + 8 * r) * 8 + 4 * i + c);
+      ks[r] = __ldg(p.ks + row + g + 8 * r);
+    }
+  }
+  __device__ __forceinline__ void load_v(const PagedPool& p, long long row, int g, int c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      v[s] = __ldg(reinterpret_cast<const uint4*>(p.v) + (row + 2 * c + (s & 1) + 8 * (s >> 1)) * 8 + g);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) vs[r] = __ldg(p.vs + row + g + 8 * r);
+  }
+};
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ void set_word(uint4& v, int i, uint32_t w) {
+  if (i == 0) v.x = w;
+  else if (i == 1) v.y = w;
+  else if (i == 2) v.z = w;
+  else v.w = w;
+}
+
+// Values of a group that only some of the tile's rows see: an infinity or NaN
+// times a zero weight would reach the rows that do not see it, so it is taken
+// out (set to zero) and its key remembered per dim; rows whose limit is past
+// that key get NaN at the end. Rare: any non-finite value at all ends in NaNs.
+__device__ __noinline__ void note_poison(int* poison, int dim, int key) { atomicMin(poison + dim, key); }
+
+template <bool kE4m3>
+__device__ __forceinline__ void take_out_poison(KvGroup<kE4m3>& kv, int* poison, int key0, int g, int c) {
+  if constexpr (!kE4m3) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w = word(kv.v[s][j], i);
+          const int key = key0 + 2 * c + (s & 1) + 8 * (s >> 1);
+          const int dim = 64 * j + 8 * g + 2 * i;
+          if ((w & 0x7f80u) == 0x7f80u) {
+            note_poison(poison, dim, key);
+            w &= 0xffff0000u;
+          }
+          if ((w & 0x7f800000u) == 0x7f800000u) {
+            note_poison(poison, dim + 1, key);
+            w &= 0xffffu;
+          }
+          set_word(kv.v[s][j], i, w);
+        }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (kv.vs[r] == 255u) {
+        for (int d = 0; d < 32; ++d) note_poison(poison, 32 * c + d, key0 + g + 8 * r);
+        kv.vs[r] = 0u;
+      }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w = word(kv.v[s], i);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (((w >> (8 * b)) & 0x7fu) == 0x7fu) {
+            note_poison(poison, 16 * g + 4 * i + b, key0 + 2 * c + (s & 1) + 8 * (s >> 1));
+            w &= ~(0xffu << (8 * b));
+          }
+        set_word(kv.v[s], i, w);
+      }
+  }
+}
+
+// keys at or behind `live` (counted from the group's first): their values are
+// whatever the page holds there, and become zero
+template <bool kE4m3>
+__device__ __forceinline__ void clear_tail(KvGroup<kE4m3>& kv, int live, int g, int c) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    if (2 * c + (s & 1) + 8 * (s >> 1) >= live) {
+      if constexpr (kE4m3)
+        kv.v[s] = make_uint4(0, 0, 0, 0);
+      else
+        kv.v[s][0] = kv.v[s][1] = make_uint4(0, 0, 0, 0);
+    }
+  if constexpr (kE4m3)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (g + 8 * r >= live) kv.vs[r] = 0u;
+}
+
+// Attention of up to 8 query rows per unit over a range of keys; bound by the
+// bytes of the pages. Each warp takes 16 keys at a time straight into
+// registers (no shared memory, no barrier in the loop) and keeps its own running
+// max, sum and O^T; the warps' results are merged through shared memory, the
+// ranges' results by whichever CTA arrives last, in the order of the ranges.
+// Tensor-core shapes: S^T (16 keys x 8 rows) = K Q^T and O^T (128 dims x 8
+// rows) += V^T P^T, so the keys and values are the 16-row operand and no row is
+// wasted on padding to 16 query rows; P^T gets into operand layout by
+// movmatrix. bf16 pages: P is split into two bf16 (hi + lo), whose products sum
+// in f32, so that the weights are not rounded to 8 bits. e4m3 pages: keys and values become f16 exactly, the
+// scales are applied in f32 to the scores and to the weights (relative to the
+// largest value scale so far, so that a weight in f16 neither overflows nor
+// loses the keys that count); queries are scaled by a power of two into f16.
+template <bool kE4m3>
+__global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(const __grid_constant__ PagedAttnParams p) {
+  __shared__ float s_o[kSmallWarps][kSmallRows][132];
+  __shared__ float2 s_ml[kSmallWarps][kSmallRows];
+  __shared__ int s_poison[128];
+  __shared__ int s_last;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int warp = warp_id(), lane = lane_id(), g = lane >> 2, c = lane & 3;
+  const int page_mask = (1 << p.page_shift) - 1;
+  const int u_end = p.cta_unit0[blockIdx.x + 1];
+  for (int u = p.cta_unit0[blockIdx.x]; u < u_end; ++u) {
+    const PagedUnit un = p.units[u];
+    const int q0 = p.seq_q0[un.seq], q_len = p.seq_q0[un.seq + 1] - q0, kv_len = p.seq_kv[un.seq];
+    const int vis = p.seq_vis[un.seq];
+    const int* pages = p.pages + p.seq_page0[un.seq];
+    const int rows = min(kSmallRows, q_len * p.group - un.row0);
+    const int past = kv_len - q_len;
+    auto limit_of = [&](int r) { return max(vis, past + (un.row0 + min(r, rows - 1)) / p.group + 1); };
+    const int lim_min = limit_of(0), lim_max = limit_of(rows - 1);
+    const int lim[2] = {limit_of(2 * c), limit_of(2 * c + 1)};
+    for (int i = threadIdx.x; i < 128; i += kSmallWarps * 32) s_poison[i] = INT_MAX;
+    __syncthreads();
+
+    // this lane's piece of query row g, in the dims order of the key registers
+    uint32_t q[16];
+    float qf[2] = {p.scale_log2, p.scale_log2};  // score factor of rows 2c, 2c + 1
+    {
+      const int rr = un.row0 + g;
+      const bool live = g < rows;
+      const uint4* src = p.q + (static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group) * 16;
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int piece = kE4m3 ? 8 * (i >> 1) + 2 * c + (i & 1) : 4 * i + c;
+        w[i] = live ? __ldg(src + piece) : make_uint4(0, 0, 0, 0);
+      }
+      if (!kE4m3) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = word(w[i >> 2], i & 3);
+      } else {
+        float f[4][8];
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          unpack_bf16x8(w[i], f[i]);
+          m = fmax3_nan(m, amax8(f[i]), 0.f);
+        }
+        m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.f);
+        m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, 2), 0.f);
+        // 2^x with |q| / 2^x < 2; rows of zeros, of f32 subnormals or with a non-finite value stay as they are
+        const uint32_t ex = (__float_as_uint(m) >> 23) & 255u;
+        const bool plain = ex == 0u || ex == 255u;
+        const float down = plain ? 1.f : __uint_as_float(max(1u, 254u - ex) << 23);
+        const float up = plain ? 1.f : __uint_as_float(ex << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = pack_half2(f[i >> 2][2 * (i & 3)] * down, f[i >> 2][2 * (i & 3) + 1] * down);
+        qf[0] *= __shfl_sync(0xffffffffu, up, 8 * c);      // row 2c is lane group g = 2c
+        qf[1] *= __shfl_sync(0xffffffffu, up, 8 * c + 4);
+      }
+    }
+
+    float o[8][4];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    int v_ref = 0;  // largest value scale byte so far (e4m3)
+
+    KvGroup<kE4m3> kv;
+    const int key_last = un.key1;
+    int key = un.key0 + warp * kSmallGroup;
+    auto row_of = [&](int k) {
+      return ((static_cast<long long>(pages[k >> p.page_shift]) * p.Hkv + un.head) << p.page_shift) + (k & page_mask);
+    };
+    long long row = 0;
+    if (key < key_last) {
+      row = row_of(key);
+      kv.load_k(p.pool, row, g, c);
+      kv.load_v(p.pool, row, g, c);
+    }
+    while (key < key_last) {
+      const int next = key + kSmallWarps * kSmallGroup;
+      const long long row_next = next < key_last ? row_of(next) : 0;
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float kf[2] = {1.f, 1.f};
+      if constexpr (!kE4m3) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mma_16816<true>(s, kv.k[0][i].x, kv.k[1][i].x, kv.k[0][i].y, kv.k[1][i].y, q[4 * i], q[4 * i + 1]);
+          mma_16816<true>(s, kv.k[0][i].z, kv.k[1][i].z, kv.k[0][i].w, kv.k[1][i].w, q[4 * i + 2], q[4 * i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t a = word(kv.k[0][i], h), b = word(kv.k[1][i], h);
+            mma_16816<false>(s, e4m3x2_f16x2(a), e4m3x2_f16x2(b), e4m3x2_f16x2(a >> 16), e4m3x2_f16x2(b >> 16),
+                             q[8 * i + 2 * h], q[8 * i + 2 * h + 1]);
+          }
+        kf[0] = e8m0_value(kv.ks[0]);
+        kf[1] = e8m0_value(kv.ks[1]);
+      }
+      if (next < key_last) kv.load_k(p.pool, row_next, g, c);
+      // base-2 scores; s[0], s[1]: key g, rows 2c, 2c + 1; s[2], s[3]: key g + 8
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = s[i] * (kE4m3 ? qf[i & 1] * kf[i >> 1] : qf[i & 1]);
+      const bool whole = key + kSmallGroup <= lim_min;
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (key + g + 8 * (i >> 1) >= lim[i & 1]) x[i] = -INFINITY;
+        clear_tail<kE4m3>(kv, lim_max - key, g, c);
+        if (lim_max != lim_min) take_out_poison<kE4m3>(kv, s_poison, key, g, c);
+      }
+      // the running max moves only when a score passes it by 2^8
+      const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+      bool grow = mx0 > m_run[0] + kLazyRescaleLog2 || mx1 > m_run[1] + kLazyRescaleLog2;
+      int v_max = 0;
+      if constexpr (kE4m3) {
+        v_max = static_cast<int>(max(kv.vs[0], kv.vs[1]));
+        grow = grow || v_max > v_ref;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        float a[2] = {mx0, mx1}, f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], d));
+          a[i] = fmaxf(a[i], m_run[i]);
+          f[i] = ex2_approx(m_run[i] - finite_or_zero(a[i]));
+          m_run[i] = a[i];
+          l_run[i] *= f[i];
+        }
+        if constexpr (kE4m3) {
+          v_max = max(v_ref, __reduce_max_sync(0xffffffffu, v_max));
+          const float d = ex2_approx(static_cast<float>(v_ref - v_max));
+          f[0] *= d;
+          f[1] *= d;
+          v_ref = v_max;
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[t][i] *= f[i & 1];
+      }
+      const float m0 = finite_or_zero(m_run[0]), m1 = finite_or_zero(m_run[1]);
+      float pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(x[i] - ((i & 1) ? m1 : m0));
+      l_run[0] += pr[0] + pr[2];
+      l_run[1] += pr[1] + pr[3];
+      if constexpr (!kE4m3) {
+        const uint32_t h0 = pack_bf162(pr[0], pr[1]), h1 = pack_bf162(pr[2], pr[3]);
+        const uint32_t l0 = pack_bf162(pr[0] - __uint_as_float(h0 << 16), pr[1] - __uint_as_float(h0 & 0xffff0000u));
+        const uint32_t l1 = pack_bf162(pr[2] - __uint_as_float(h1 << 16), pr[3] - __uint_as_float(h1 & 0xffff0000u));
+        const uint32_t b0 = transpose_8x8(h0), b1 = transpose_8x8(h1);
+        const uint32_t d0 = transpose_8x8(l0), d1 = transpose_8x8(l1);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const uint32_t sel = (t & 1) ? 0x7632u : 0x5410u;
+          uint32_t a[4];  // dims 8g + t and 64 + 8g + t; keys 2c, 2c+1 and 2c+8, 2c+9
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            a[j] = __byte_perm(word(kv.v[0][j], t >> 1), word(kv.v[1][j], t >> 1), sel);
+            a[2 + j] = __byte_perm(word(kv.v[2][j], t >> 1), word(kv.v[3][j], t >> 1), sel);
+          }
+          mma_16816<true>(o[t], a[0], a[1], a[2], a[3], b0, b1);
+          mma_16816<true>(o[t], a[0], a[1], a[2], a[3], d0, d1);
+        }
+      } else {
+        float w[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float f = ex2_approx(static_cast<float>(static_cast<int>(kv.vs[r]) - v_ref));
+          w[2 * r] = pr[2 * r] * f;
+          w[2 * r + 1] = pr[2 * r + 1] * f;
+        }
+        const uint32_t b0 = transpose_8x8(pack_half2(w[0], w[1])), b1 = transpose_8x8(pack_half2(w[2], w[3]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // word i of the low and of the high half: dims 16g + 4i.. and 16g + 8 + 4i..
+          uint32_t e[2][2][2];  // [dim half][key pair][dims 0,1 | 2,3]: bytes (key a, key b) per dim
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int kp = 0; kp < 2; ++kp) {
+              const uint32_t a = word(kv.v[2 * kp], 2 * j + i), b = word(kv.v[2 * kp + 1], 2 * j + i);
+              e[j][kp][0] = __byte_perm(a, b, 0x5140);
+              e[j][kp][1] = __byte_perm(a, b, 0x7362);
+            }
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const int sh = 16 * (d & 1);
+            mma_16816<false>(o[4 * i + d], e4m3x2_f16x2(e[0][0][d >> 1] >> sh), e4m3x2_f16x2(e[1][0][d >> 1] >> sh),
+                             e4m3x2_f16x2(e[0][1][d >> 1] >> sh), e4m3x2_f16x2(e[1][1][d >> 1] >> sh), b0, b1);
+          }
+        }
+      }
+      if (next < key_last) kv.load_v(p.pool, row_next, g, c);
+      key = next;
+    }
+
+    // merge of the warps
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], d);
+    }
+    const float unscale = kE4m3 ? e8m0_value(static_cast<uint32_t>(v_ref)) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 2 * c + i;
+      if (g == 0) s_ml[warp][r] = make_float2(m_run[i], l_run[i]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float* dst = &s_o[warp][r][kE4m3 ? 16 * g + 8 * j : 64 * j + 8 * g];
+#pragma unroll
+        for (int t = 0; t < 8; t += 4)
+          *reinterpret_cast<float4*>(dst + t) = make_float4(o[t][2 * j + i] * unscale, o[t + 1][2 * j + i] * unscale,
+                                                            o[t + 2][2 * j + i] * unscale, o[t + 3][2 * j + i] * unscale);
+      }
+    }
+    __syncthreads();
+    const int nsplit = un.split >> 16, split = un.split & 0xffff;
+    const int r = warp;  // one warp per row
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float2 ml, const float4 v) {
+      const float w = ex2_approx(ml.x - finite_or_zero(m));
+      l = fmaf(ml.y, w, l);
+      acc.x = fmaf(v.x, w, acc.x);
+      acc.y = fmaf(v.y, w, acc.y);
+      acc.z = fmaf(v.z, w, acc.z);
+      acc.w = fmaf(v.w, w, acc.w);
+    };
+    if (r < rows) {
+#pragma unroll
+      for (int i = 0; i < kSmallWarps; ++i) m = fmaxf(m, s_ml[i][r].x);
+#pragma unroll
+      for (int i = 0; i < kSmallWarps; ++i) add(s_ml[i][r], *reinterpret_cast<const float4*>(&s_o[i][r][4 * lane]));
+      if (lim_max != lim_min) {
+        const int lr = limit_of(r);
+        if (s_poison[4 * lane] < lr) acc.x = NAN;
+        if (s_poison[4 * lane + 1] < lr) acc.y = NAN;
+        if (s_poison[4 * lane + 2] < lr) acc.z = NAN;
+        if (s_poison[4 * lane + 3] < lr) acc.w = NAN;
+      }
+    }
+    bool write = r < rows;
+    if (nsplit > 1) {
+      if (r < rows) {
+        float* slot = p.part + static_cast<long long>(un.slot0 + split) * kSmallSlot;
+        reinterpret_cast<float4*>(slot + r * 128)[lane] = acc;
+        if (lane == 0) reinterpret_cast<float2*>(slot + kSmallRows * 128)[r] = make_float2(m, l);
+      }
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        // wraps to 0 with the last arrival: ready for the next call
+        s_last = atomicInc(reinterpret_cast<unsigned*>(p.counters) + un.counter, nsplit - 1) == nsplit - 1;
+        __threadfence();
+      }
+      __syncthreads();
+      write = write && s_last;
+      if (write) {
+        const float* slot = p.part + static_cast<long long>(un.slot0) * kSmallSlot;
+        float mm = -INFINITY;
+        for (int i = lane; i < nsplit; i += 32)
+          mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(slot + static_cast<long long>(i) * kSmallSlot + kSmallRows * 128) + r).x);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+        m = mm;
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < nsplit; ++i) {
+          const float* sl = slot + static_cast<long long>(i) * kSmallSlot;
+          add(__ldcg(reinterpret_cast<const float2*>(sl + kSmallRows * 128) + r), __ldcg(reinterpret_cast<const float4*>(sl + r * 128) + lane));
+        }
+      }
+    }
+    if (write) {
+      const int rr = un.row0 + r;
+      const long long out_row = static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
+      const float inv = 1.0f / l;
+      reinterpret_cast<uint2*>(p.o + out_row * 16)[lane] = make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
+      if (p.lse && lane == 0) p.lse[out_row] = lse_of(m, l);
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace mot
