@@ -116,6 +116,11 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
                                const int32_t* visible, const int32_t* table, int32_t table_stride, int32_t n_pages,
                                void* stream);
 
+/* What mot_paged_batch_set refuses in its arguments. Host-only; no CUDA calls. */
+mot_status mot_paged_batch_check(const mot_paged_config* cfg, int32_t batch, const int32_t* q_len,
+                                 const int32_t* kv_len, const int32_t* visible, const int32_t* table,
+                                 int32_t table_stride, int32_t n_pages);
+
 /* Device workspace bytes mot_paged_attend needs for any batch of this object. */
 mot_status mot_paged_query_workspace(mot_paged_batch_t bt, size_t* workspace_bytes);
 

@@ -146,6 +146,10 @@ SIGNATURES = {
     "mot_paged_batch_create": (c_int32, [c_void_p, POINTER(c_void_p)]),
     "mot_paged_batch_set": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
                                       c_void_p]),
+    "mot_paged_batch_check": (c_int32, [POINTER(MotPagedConfig), c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_int32, c_int32]),
+    "mot_dev_paged_plan": (c_int32, [c_int32, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p,
+                                     c_void_p]),
     "mot_paged_query_workspace": (c_int32, [c_void_p, POINTER(c_size_t)]),
     "mot_paged_append": (c_int32, [c_void_p, c_void_p, c_void_p, POINTER(MotPagedPoolC), c_void_p, c_void_p]),
     "mot_paged_store": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, POINTER(MotPagedPoolC), c_void_p]),

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmotattn.so")
 SOURCES = ["mot_attn.cu"]
 HEADERS = ["ptx.cuh", "gemm.cuh", "attn_fwd.cuh", "attn_bwd.cuh", "aux.cuh", "mot_mlp.cuh", "mot_step.cuh", "moe.cuh", "mot_moe.cuh",
-           "paged.cuh", "mot_paged.cuh"]
+           "paged.cuh", "paged_tile.cuh", "mot_paged.cuh"]
 
 
 def nvcc_path() -> str:

@@ -5,17 +5,19 @@
 //   append   norm + rotation + cache write of the chunk
 //   store    dense cache -> pages
 //   load     pages -> dense cache
-//   attend   attention units cut over the SMs by mot_paged_batch_set
+//   attend   attention units cut over the SMs by mot_paged_batch_set: one
+//            launch for the sequences with few query rows, one for the others
 #pragma once
 
 #include "mot_paged.h"
 #include "paged.cuh"
+#include "paged_tile.cuh"
 
 struct mot_paged {
   mot_paged_config cfg;
   int device = 0;
   int num_sms = 148;
-  int small_ctas = 0;      // grid of the few-rows attention
+  int ctas[2] = {0, 0};    // grids of the few-rows and of the 256-row attention
   float* gains = nullptr;  // q_norm [128], k_norm [128]
   float2* rope = nullptr;  // [max_positions, 64]
   int* status = nullptr;
@@ -23,17 +25,20 @@ struct mot_paged {
 
 namespace {
 
-constexpr int kPagedGranule = kSmallWarps * kSmallGroup;  // keys: one 16-key group for every warp of a CTA
-
 // Device tables of a batch object, at fixed offsets (32-bit words) so that a
-// captured call finds them after the batch is set again.
+// captured call finds them after the batch is set again. [0]: the few-rows
+// attention, [1]: the 256-row one.
 struct PagedTables {
-  size_t counters, cta_unit0, n_entries, seq_q0, seq_kv, seq_vis, seq_page0, head_words;  // one block, one copy
-  size_t pages, page_seq, tok, units, words;
-  int unit_cap;
+  size_t counters[2], cta_unit0[2], n_entries, seq_q0, seq_kv, seq_vis, seq_page0, head_words;  // one block, one copy
+  size_t pages, page_seq, tok, units[2], words;
+  int unit_cap[2];
 };
 
-PagedTables paged_tables(const mot_paged_config& c, int ctas) {
+// Query rows (tokens times heads of the group) up to which a sequence goes to
+// the few-rows kernel.
+constexpr int kSmallMaxRows = 2 * kSmallRows;
+
+PagedTables paged_tables(const mot_paged_config& c, const int (&ctas)[2]) {
   PagedTables t;
   size_t off = 0;
   auto take = [&](size_t words) {
@@ -42,8 +47,8 @@ PagedTables paged_tables(const mot_paged_config& c, int ctas) {
     return o;
   };
   const size_t B = c.max_batch, T = c.max_tokens, G = c.n_q_heads / c.n_kv_heads;
-  t.counters = take(ctas);
-  t.cta_unit0 = take(ctas + 1);
+  for (int i = 0; i < 2; ++i) t.counters[i] = take(ctas[i]);
+  for (int i = 0; i < 2; ++i) t.cta_unit0[i] = take(ctas[i] + 1);
   t.n_entries = take(1);
   t.seq_q0 = take(B + 1);
   t.seq_kv = take(B);
@@ -53,9 +58,12 @@ PagedTables paged_tables(const mot_paged_config& c, int ctas) {
   t.pages = take(c.max_pages);
   t.page_seq = take(c.max_pages);
   t.tok = take(2 * T);
-  const size_t tiles = T * G / kSmallRows + std::min(B, T);
-  t.unit_cap = static_cast<int>(tiles * c.n_kv_heads + ctas);
-  t.units = take(static_cast<size_t>(t.unit_cap) * (sizeof(PagedUnit) / 4));
+  const size_t seqs = std::min(B, T);
+  const size_t tiles[2] = {seqs * (kSmallMaxRows / kSmallRows), T * G / kTileRows + seqs};
+  for (int i = 0; i < 2; ++i) {
+    t.unit_cap[i] = static_cast<int>(tiles[i] * c.n_kv_heads + ctas[i]);  // every cut makes one more
+    t.units[i] = take(static_cast<size_t>(t.unit_cap[i]) * (sizeof(PagedUnit) / 4));
+  }
   t.words = off;
   return t;
 }
@@ -93,7 +101,7 @@ struct mot_paged_batch {
   std::vector<uint8_t> times;
   uint32_t set_no = 0;
   // what the last set described
-  int batch = 0, tokens = 0, entries = 0, n_pages = 0, kv_max = 0, units = 0;
+  int batch = 0, tokens = 0, entries = 0, n_pages = 0, kv_max = 0, units[2] = {0, 0};
   bool repeated = false, repeated_written = false;
 };
 
@@ -105,43 +113,48 @@ int log2_of(int v) {
   return s;
 }
 
-// Cuts the attention's tiles (sequence, KV head, 8 query rows), each with its
-// own number of keys, over the CTAs: the CTAs take equal shares of the total
-// work in tile order, a tile that straddles a boundary is split there (at a
-// multiple of kPagedGranule keys) and its ranges merged on the device. The
-// share is the smallest that fits; work is counted in granules, a unit's
-// prologue and merge as kUnitCost of them.
-constexpr int kUnitCost = 1, kMinShare = 3;
+// How the attention's tiles -- (sequence, KV head, query rows), each with its
+// own number of keys -- are cut over the CTAs: the CTAs take equal shares of the
+// work in tile order; a tile that straddles a boundary is split there, at a
+// multiple of `granule` keys, and its ranges are merged on the device. Work is
+// counted in granules, a unit's prologue and merge as `unit_cost` of them.
+struct CutRule {
+  int granule, unit_cost, min_share;
+};
+constexpr CutRule kCutRules[2] = {{kSmallWarps * kSmallGroup, 1, 3}, {kTileKeys, 2, 4}};
 
-struct SmallTile {
-  int seq, row0, granules, keys;
+struct PagedTile {
+  int seq, row0, keys;
 };
 
-int cut_units(const std::vector<SmallTile>& tiles, int heads, int ctas, int share, PagedUnit* units, int unit_cap,
-              int* cta_unit0, int* n_units) {
-  int cta = 0, load = 0, n = 0, slots = 0, counters = 0;
+// One pass with a given share; returns whether it fits. Without `cut` the tiles
+// stay whole. `units` null: only the test.
+bool cut_units(const std::vector<PagedTile>& tiles, int heads, int ctas, long long share, bool cut, const CutRule& rule,
+               PagedUnit* units, int unit_cap, int* cta_unit0, int* n_units) {
+  int cta = 0, n = 0, slots = 0, counters = 0;
+  long long load = 0;
   if (cta_unit0) cta_unit0[0] = 0;
-  for (const SmallTile& tl : tiles)
+  for (const PagedTile& tl : tiles) {
+    const int granules = (tl.keys + rule.granule - 1) / rule.granule;
     for (int head = 0; head < heads; ++head) {
       const int first = n;
       int at = 0;
-      while (at < tl.granules) {
-        int room = share - load - kUnitCost;
-        if (room < 1 && load > 0) {
-          if (++cta >= ctas) return -1;
+      while (at < granules) {
+        const long long room = share - load - rule.unit_cost;
+        if (load > 0 && (cut ? room < 1 : room < granules)) {
+          if (++cta >= ctas) return false;
           if (cta_unit0) cta_unit0[cta] = n;
           load = 0;
           continue;
         }
-        room = std::max(room, 1);
-        int take = std::min(room, tl.granules - at);
+        const int take = cut ? static_cast<int>(std::min<long long>(std::max<long long>(room, 1), granules - at)) : granules;
         if (units) {
-          if (n >= unit_cap) return -1;
-          units[n] = PagedUnit{tl.seq, head, tl.row0, at * kPagedGranule, std::min(tl.keys, (at + take) * kPagedGranule), 0, 0, 0};
+          if (n >= unit_cap) return false;
+          units[n] = PagedUnit{tl.seq, head, tl.row0, at * rule.granule, std::min(tl.keys, (at + take) * rule.granule), 0, 0, 0};
         }
         ++n;
         at += take;
-        load += take + kUnitCost;
+        load += take + rule.unit_cost;
       }
       const int pieces = n - first;
       if (units)
@@ -155,10 +168,37 @@ int cut_units(const std::vector<SmallTile>& tiles, int heads, int ctas, int shar
         ++counters;
       }
     }
+  }
   if (cta_unit0)
     for (int i = cta + 1; i <= ctas; ++i) cta_unit0[i] = n;
   if (n_units) *n_units = n;
-  return cta + 1;
+  return true;
+}
+
+// The smallest share that fits, whole tiles where that costs at most 1/16 more.
+bool plan_units(const std::vector<PagedTile>& tiles, int heads, int ctas, const CutRule& rule, PagedUnit* units,
+                int unit_cap, int* cta_unit0, int* n_units) {
+  long long total = 0, largest = 0;
+  for (const PagedTile& tl : tiles) {
+    const long long w = (tl.keys + rule.granule - 1) / rule.granule + rule.unit_cost;
+    total += w * heads;
+    largest = std::max(largest, w);
+  }
+  auto smallest = [&](bool cut) {
+    long long lo = std::max<long long>(cut ? rule.min_share : largest, (total + ctas - 1) / ctas);
+    long long hi = std::max(lo, total + 1);
+    while (lo < hi) {
+      const long long mid = lo + (hi - lo) / 2;
+      if (cut_units(tiles, heads, ctas, mid, cut, rule, nullptr, 0, nullptr, nullptr))
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    return lo;
+  };
+  const long long cut_share = smallest(true), whole_share = smallest(false);
+  const bool cut = whole_share > cut_share + cut_share / 16;
+  return cut_units(tiles, heads, ctas, cut ? cut_share : whole_share, cut, rule, units, unit_cap, cta_unit0, n_units);
 }
 
 bool paged_device_ok(const mot_paged* h) {
@@ -226,18 +266,19 @@ mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights
   if (!h) return MOT_ERR_CUDA;
   h->cfg = *cfg;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cfg->kv_dtype == MOT_PAGED_E4M3;
+  set_smem_attr(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, TileSmem::kBytes);
   int per_sm = 0;
   bool ok = cudaGetDevice(&h->device) == cudaSuccess &&
             cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) == cudaSuccess &&
-            (cfg->kv_dtype == MOT_PAGED_E4M3
-                 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_attn_small_kernel<true>, kSmallWarps * 32, 0)
-                 : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_attn_small_kernel<false>, kSmallWarps * 32, 0)) ==
-                cudaSuccess &&
-            per_sm > 0 && cudaMalloc(&h->gains, 256 * sizeof(float)) == cudaSuccess &&
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>,
+                                                          kSmallWarps * 32, 0) == cudaSuccess &&
+            per_sm > 0 && encode_ready() && cudaMalloc(&h->gains, 256 * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&h->rope, static_cast<size_t>(cfg->max_positions) * 64 * sizeof(float2)) == cudaSuccess &&
             cudaMalloc(&h->status, sizeof(int)) == cudaSuccess;
   if (ok) {
-    h->small_ctas = per_sm * h->num_sms;
+    h->ctas[0] = per_sm * h->num_sms;
+    h->ctas[1] = h->num_sms;
     RopeFreq f;
     for (int j = 0; j < 64; ++j) f.inv[j] = std::pow(cfg->rope_theta, -2.0 * j / 128.0);
     bf16_to_f32_kernel<<<1, 128, 0, s>>>(static_cast<const __nv_bfloat16*>(w->q_norm), h->gains, 128);
@@ -263,7 +304,7 @@ mot_status mot_paged_batch_create(mot_paged_t h, mot_paged_batch_t* out) {
   mot_paged_batch* bt = new (std::nothrow) mot_paged_batch();
   if (!bt) return MOT_ERR_CUDA;
   bt->h = h;
-  bt->t = paged_tables(h->cfg, h->small_ctas);
+  bt->t = paged_tables(h->cfg, h->ctas);
   bool ok = true;
   try {
     bt->host.resize(bt->t.words);
@@ -285,21 +326,21 @@ void mot_paged_batch_destroy(mot_paged_batch_t bt) {
   delete bt;
 }
 
-mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_t* q_len, const int32_t* kv_len,
-                               const int32_t* visible, const int32_t* table, int32_t table_stride, int32_t n_pages,
-                               void* stream) {
-  if (!bt || !q_len || !kv_len || batch <= 0 || table_stride < 0 || n_pages <= 0) return MOT_ERR_INVALID_ARGUMENT;
-  mot_paged* h = bt->h;
-  const mot_paged_config& c = h->cfg;
-  if (batch > c.max_batch) return MOT_ERR_UNSUPPORTED_SHAPE;
-  const int shift = log2_of(c.page_size);
+mot_status mot_paged_batch_check(const mot_paged_config* cfg, int32_t batch, const int32_t* q_len,
+                                 const int32_t* kv_len, const int32_t* visible, const int32_t* table,
+                                 int32_t table_stride, int32_t n_pages) {
+  const mot_status st = check_paged_config(cfg);
+  if (st != MOT_OK) return st;
+  if (!q_len || !kv_len || batch <= 0 || table_stride < 0 || n_pages <= 0) return MOT_ERR_INVALID_ARGUMENT;
+  if (batch > cfg->max_batch) return MOT_ERR_UNSUPPORTED_SHAPE;
+  // rows of the pool, as TMA coordinates count them
+  if (static_cast<long long>(n_pages) * cfg->n_kv_heads * cfg->page_size > INT_MAX) return MOT_ERR_UNSUPPORTED_SHAPE;
   long long tokens = 0, entries = 0;
-  int kv_max = 0;
   for (int b = 0; b < batch; ++b) {
     if (q_len[b] < 0 || kv_len[b] < q_len[b]) return MOT_ERR_INVALID_ARGUMENT;
     if (visible && (visible[b] < 0 || visible[b] > kv_len[b])) return MOT_ERR_INVALID_ARGUMENT;
-    if (kv_len[b] > c.max_positions) return MOT_ERR_UNSUPPORTED_SHAPE;
-    const int used = (kv_len[b] + c.page_size - 1) >> shift;
+    if (kv_len[b] > cfg->max_positions) return MOT_ERR_UNSUPPORTED_SHAPE;
+    const int used = (kv_len[b] + cfg->page_size - 1) / cfg->page_size;
     if (used > table_stride || (used > 0 && !table)) return MOT_ERR_INVALID_ARGUMENT;
     for (int i = 0; i < used; ++i) {
       const int id = table[static_cast<size_t>(b) * table_stride + i];
@@ -307,9 +348,26 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
     }
     tokens += q_len[b];
     entries += used;
+  }
+  return tokens > cfg->max_tokens || entries > cfg->max_pages ? MOT_ERR_UNSUPPORTED_SHAPE : MOT_OK;
+}
+
+mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_t* q_len, const int32_t* kv_len,
+                               const int32_t* visible, const int32_t* table, int32_t table_stride, int32_t n_pages,
+                               void* stream) {
+  if (!bt) return MOT_ERR_INVALID_ARGUMENT;
+  mot_paged* h = bt->h;
+  const mot_paged_config& c = h->cfg;
+  const mot_status cs = mot_paged_batch_check(&c, batch, q_len, kv_len, visible, table, table_stride, n_pages);
+  if (cs != MOT_OK) return cs;
+  const int shift = log2_of(c.page_size);
+  long long tokens = 0, entries = 0;
+  int kv_max = 0;
+  for (int b = 0; b < batch; ++b) {
+    tokens += q_len[b];
+    entries += (kv_len[b] + c.page_size - 1) >> shift;
     kv_max = std::max(kv_max, kv_len[b]);
   }
-  if (tokens > c.max_tokens || entries > c.max_pages) return MOT_ERR_UNSUPPORTED_SHAPE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
   if (!paged_device_ok(h)) return MOT_ERR_INVALID_ARGUMENT;
@@ -318,13 +376,13 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
     return MOT_ERR_INVALID_ARGUMENT;
   }
   const PagedTables& t = bt->t;
-  int n_units = 0;
+  int n_units[2] = {0, 0};
   try {
     if (bt->stamp.size() < static_cast<size_t>(n_pages)) {
       bt->stamp.resize(n_pages, 0u);
       bt->times.resize(n_pages, 0);
     }
-    std::vector<SmallTile> tiles;
+    std::vector<PagedTile> tiles[2];
     bt->batch = 0;  // nothing is described until the copies below are enqueued
     ++bt->set_no;
     int* w = bt->host.data();
@@ -355,10 +413,10 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
         w[t.tok + 2 * (q0 + i)] = pos;
         w[t.tok + 2 * (q0 + i) + 1] = row[pos >> shift];
       }
-      for (int r = 0; r < q_len[b] * group; r += kSmallRows) {
-        const int last = std::min(q_len[b] * group, r + kSmallRows) - 1;
-        const int keys = std::max(w[t.seq_vis + b], past + last / group + 1);
-        tiles.push_back(SmallTile{b, r, (keys + kPagedGranule - 1) / kPagedGranule, keys});
+      const int rows = q_len[b] * group, kind = rows <= kSmallMaxRows ? 0 : 1, step = kind ? kTileRows : kSmallRows;
+      for (int r = 0; r < rows; r += step) {
+        const int last = std::min(rows, r + step) - 1;
+        tiles[kind].push_back(PagedTile{b, r, std::max(w[t.seq_vis + b], past + last / group + 1)});
       }
       q0 += q_len[b];
       e0 += used;
@@ -373,23 +431,12 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
         if (q_len[b] > 0)
           for (int i = (kv_len[b] - q_len[b]) >> shift; i <= (kv_len[b] - 1) >> shift; ++i)
             bt->repeated_written |= bt->times[table[static_cast<size_t>(b) * table_stride + i]] > 1;
-    // smallest share per CTA that fits
-    long long total = 0;
-    for (const SmallTile& tl : tiles) total += static_cast<long long>(tl.granules + kUnitCost) * c.n_kv_heads;
-    const int ctas = h->small_ctas;
-    long long lo = std::max<long long>(kMinShare, (total + ctas - 1) / ctas), hi = std::max<long long>(lo, total + 1);
-    if (hi > INT_MAX) return MOT_ERR_UNSUPPORTED_SHAPE;
-    while (lo < hi) {
-      const long long mid = lo + (hi - lo) / 2;
-      if (cut_units(tiles, c.n_kv_heads, ctas, static_cast<int>(mid), nullptr, 0, nullptr, nullptr) > 0)
-        hi = mid;
-      else
-        lo = mid + 1;
+    for (int i = 0; i < 2; ++i) {
+      std::fill(w + t.counters[i], w + t.counters[i] + h->ctas[i], 0);
+      if (!plan_units(tiles[i], c.n_kv_heads, h->ctas[i], kCutRules[i], reinterpret_cast<PagedUnit*>(w + t.units[i]),
+                      t.unit_cap[i], w + t.cta_unit0[i], &n_units[i]))
+        return MOT_ERR_UNSUPPORTED_SHAPE;
     }
-    std::fill(w + t.counters, w + t.counters + ctas, 0);
-    if (cut_units(tiles, c.n_kv_heads, ctas, static_cast<int>(lo), reinterpret_cast<PagedUnit*>(w + t.units), t.unit_cap,
-                  w + t.cta_unit0, &n_units) < 0)
-      return MOT_ERR_UNSUPPORTED_SHAPE;
   } catch (...) {
     return MOT_ERR_CUDA;
   }
@@ -397,7 +444,8 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
                               {t.pages, static_cast<size_t>(entries)},
                               {t.page_seq, static_cast<size_t>(entries)},
                               {t.tok, static_cast<size_t>(2 * tokens)},
-                              {t.units, static_cast<size_t>(n_units) * (sizeof(PagedUnit) / 4)}};
+                              {t.units[0], static_cast<size_t>(n_units[0]) * (sizeof(PagedUnit) / 4)},
+                              {t.units[1], static_cast<size_t>(n_units[1]) * (sizeof(PagedUnit) / 4)}};
   for (const auto& pc : pieces)
     if (pc[1] > 0 && cudaMemcpyAsync(bt->dev + pc[0], bt->host.data() + pc[0], pc[1] * sizeof(int), cudaMemcpyHostToDevice,
                                      st) != cudaSuccess)
@@ -407,14 +455,16 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
   bt->entries = static_cast<int>(entries);
   bt->n_pages = n_pages;
   bt->kv_max = kv_max;
-  bt->units = n_units;
+  bt->units[0] = n_units[0];
+  bt->units[1] = n_units[1];
   return MOT_OK;
 }
 
 mot_status mot_paged_query_workspace(mot_paged_batch_t bt, size_t* workspace_bytes) {
   if (!bt || !workspace_bytes) return MOT_ERR_INVALID_ARGUMENT;
   // a cut makes at most two ranges, and there are fewer cuts than CTAs
-  *workspace_bytes = static_cast<size_t>(bt->h->small_ctas) * 2 * kSmallSlot * sizeof(float);
+  *workspace_bytes = (static_cast<size_t>(bt->h->ctas[0]) * 2 * kSmallSlot +
+                      static_cast<size_t>(bt->h->ctas[1]) * 2 * kTileSlot) * sizeof(float);
   return MOT_OK;
 }
 
@@ -478,7 +528,10 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
   mot_paged_query_workspace(bt, &need);
   if (workspace_bytes < need) return MOT_ERR_WORKSPACE_TOO_SMALL;
   const mot_paged_config& c = h->cfg;
-  PagedAttnParams p{};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = c.kv_dtype == MOT_PAGED_E4M3;
+  PagedTileParams tp{};
+  PagedAttnParams& p = tp.a;
   p.q = static_cast<const uint4*>(q);
   p.o = static_cast<uint4*>(o);
   p.lse = lse;
@@ -488,20 +541,47 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
   p.seq_vis = bt->dev + bt->t.seq_vis;
   p.seq_page0 = bt->dev + bt->t.seq_page0;
   p.pages = bt->dev + bt->t.pages;
-  p.units = reinterpret_cast<const PagedUnit*>(bt->dev + bt->t.units);
-  p.cta_unit0 = bt->dev + bt->t.cta_unit0;
-  p.counters = bt->dev + bt->t.counters;
-  p.part = static_cast<float*>(workspace);
   p.Hq = c.n_q_heads;
   p.Hkv = c.n_kv_heads;
   p.group = c.n_q_heads / c.n_kv_heads;
   p.page_shift = log2_of(c.page_size);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
   p.status = h->status;
-  auto kern = c.kv_dtype == MOT_PAGED_E4M3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>;
-  return launch_pdl(kern, dim3(h->small_ctas), dim3(kSmallWarps * 32), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess
-             ? MOT_OK
-             : MOT_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    if (bt->units[i] == 0) continue;
+    p.units = reinterpret_cast<const PagedUnit*>(bt->dev + bt->t.units[i]);
+    p.cta_unit0 = bt->dev + bt->t.cta_unit0[i];
+    p.counters = bt->dev + bt->t.counters[i];
+    p.part = static_cast<float*>(workspace) + (i ? static_cast<size_t>(h->ctas[0]) * 2 * kSmallSlot : 0);
+    if (i == 0) {
+      e = launch_pdl(e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>, dim3(h->ctas[0]),
+                     dim3(kSmallWarps * 32), 0, st, p);
+    } else {
+      const uint64_t rows = static_cast<uint64_t>(pool->n_pages) * c.n_kv_heads * c.page_size;
+      if (!e4m3 && (!map2d(&tp.k_map, pool->k, true, 128, rows, 128, c.page_size) ||
+                    !map2d(&tp.v_map, pool->v, true, 128, rows, 128, c.page_size)))
+        return MOT_ERR_CUDA;
+      e = launch_pdl(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, dim3(h->ctas[1]),
+                     dim3(kTileThreads), TileSmem::kBytes, st, tp);
+    }
+  }
+  return e == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+}
+
+mot_status mot_dev_paged_plan(int32_t kind, const int32_t* tiles, int32_t n_tiles, int32_t heads, int32_t ctas,
+                              int32_t* units, int32_t unit_cap, int32_t* cta_unit0, int32_t* n_units) {
+  if (kind < 0 || kind > 1 || (n_tiles > 0 && !tiles) || n_tiles < 0 || heads <= 0 || ctas <= 0 || !units || !cta_unit0 || !n_units)
+    return MOT_ERR_INVALID_ARGUMENT;
+  try {
+    std::vector<PagedTile> tl;
+    for (int i = 0; i < n_tiles; ++i) tl.push_back(PagedTile{tiles[3 * i], tiles[3 * i + 1], tiles[3 * i + 2]});
+    if (!plan_units(tl, heads, ctas, kCutRules[kind], reinterpret_cast<PagedUnit*>(units), unit_cap, cta_unit0, n_units))
+      return MOT_ERR_UNSUPPORTED_SHAPE;
+  } catch (...) {
+    return MOT_ERR_CUDA;
+  }
+  return MOT_OK;
 }
 
 mot_status mot_paged_get_device_status(mot_paged_t h, void* stream) {

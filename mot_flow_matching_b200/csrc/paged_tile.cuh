@@ -1,0 +1,614 @@
+// paged_tile.cuh -- attention of chunks over the pages (include/mot_paged.h,
+// mot_paged_attend) on the 5th-generation tensor cores.
+//
+// A unit is 256 query rows of one (sequence, KV head) -- (token, head of the
+// group) pairs, head fastest, as two 128-row tiles -- and a range of 128-key
+// tiles. Per key tile S_t = Q_t K^T into TMEM, softmax in registers, P_t (bf16
+// pairs) over S_t's own columns, O_t += P_t V with P_t as the TMEM operand; the
+// tensor core works on one query tile while the other's softmax runs. One CTA
+// per SM runs its list of units back to back.
+//
+// Warps 0-3 and 4-7: softmax of tile 0 and 1, one thread per query row with its
+// 128 scores in registers, so that the running max and sum need no exchange.
+// Warps 8-11: producers; bf16 pages: one TMA box per page and 64 dims (128-byte
+// swizzle, which is why page_size is a multiple of the 8-row swizzle atom),
+// issued by warp 8; e4m3 pages: 16-byte loads, each value times its row's power
+// of two into bf16 (exact) and into the same swizzled tile, so that everything
+// behind the producers is one code. Warp 12: MMA issue. The registers are split
+// by setmaxnreg: 2 x 192 + 2 x 64 of the 4 x 128 a thread the block starts with.
+//
+// Probabilities are bf16, since they meet bf16 values in one MMA: half a step
+// is 2^-9 on average below what the bf16 output itself loses; the row sum is
+// taken in f32 from the unrounded ones. The running max is raised, and O_t
+// rescaled through TMEM, only when a row's max grows by more than 2^8.
+#pragma once
+
+#include "paged.cuh"
+
+namespace mot {
+
+constexpr int kTileRows = 256;  // query rows of a unit
+constexpr int kTileKeys = 128;
+constexpr int kTileSlot = kTileRows * 128 + kTileRows * 2;  // floats of a partial
+
+struct PagedTileParams {
+  CUtensorMap k_map, v_map;  // bf16 pools: 2D {128, n_pages * Hkv * page_size}, box {64, page_size}
+  PagedAttnParams a;
+};
+
+struct TileSmem {
+  static constexpr uint32_t kTile = 32768;  // 128 rows x 128 bf16
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + 2 * kTile;
+  static constexpr uint32_t kV = kK + 2 * kTile;
+  static constexpr uint32_t kBar = kV + 2 * kTile;
+  static constexpr uint32_t kBytes = kBar + 256 + 1024;
+};
+
+constexpr int kTileThreads = 512;
+
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// 2^x for a pair of x <= 8 on the FMA pipe (x = j + f, as exp2_poly2) with a
+// degree-4 polynomial fitted here (relative error 2.7e-6): the row sums it
+// feeds stay good to f32.
+__device__ __forceinline__ void exp2_poly4(float& p0, float& p1, float x0, float x1) {
+  constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+  constexpr float c0 = 9.999992614e-01f, c1 = 6.931218140e-01f, c2 = 2.402474484e-01f, c3 = 5.591786603e-02f,
+                  c4 = 9.570103830e-03f;
+  x0 = fmaxf(x0, -125.0f);
+  x1 = fmaxf(x1, -125.0f);
+  float t0, t1, j0, j1, f0, f1, q0, q1;
+  fadd2(t0, t1, x0, x1, kShift, kShift);
+  fadd2(j0, j1, t0, t1, -kShift, -kShift);
+  fadd2(f0, f1, x0, x1, -j0, -j1);
+  ffma2(q0, q1, c4, c4, f0, f1, c3, c3);
+  ffma2(q0, q1, q0, q1, f0, f1, c2, c2);
+  ffma2(q0, q1, q0, q1, f0, f1, c1, c1);
+  ffma2(q0, q1, q0, q1, f0, f1, c0, c0);
+  p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+  p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+}
+
+// Byte offset of 16-byte piece `piece` (0..15) of row `row` in a 128 x 128 bf16
+// tile: two boxes of 64 dims, 128 bytes a row, pieces permuted by row & 7.
+__device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
+  return static_cast<uint32_t>((piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+
+// Four e4m3 (bytes of w) times 2^(b - 127) as two bf16 pairs, exactly: the byte's
+// exponent and mantissa land in the bf16 fields 2^120 too small, subnormals
+// included, and one or two multiplications by powers of two put that right
+// (f2 = 1 but for scales whose first factor would leave the bf16 range).
+struct E4m3Scale {
+  __nv_bfloat162 f1, f2;
+  bool two;
+  __device__ __forceinline__ explicit E4m3Scale(uint32_t b) {
+    two = b > 134u && b != 255u;
+    const uint32_t e1 = b == 255u ? 0x7fffu : (two ? 254u << 7 : (b + 120u) << 7);
+    const uint32_t e2 = two ? (b - 7u) << 7 : 0x3f80u;
+    const uint32_t w1 = e1 | (e1 << 16), w2 = e2 | (e2 << 16);
+    f1 = *reinterpret_cast<const __nv_bfloat162*>(&w1);
+    f2 = *reinterpret_cast<const __nv_bfloat162*>(&w2);
+  }
+};
+
+__device__ __forceinline__ uint2 e4m3x4_bf16(uint32_t w, const E4m3Scale& s) {
+  uint32_t r[2] = {__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r[i] = ((r[i] & 0x7f007f00u) >> 4) | (r[i] & 0x80008000u);
+    __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]), s.f1);
+    if (s.two) v = __hmul2(v, s.f2);
+    r[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+// a row's score max over 32 columns from col0; columns at or behind `valid` masked; NaN comes out as NaN
+template <bool kFull>
+__device__ __forceinline__ float scores_max32(const uint32_t (&s)[32], float m, int col0, int valid) {
+  float a = m, b = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = (kFull || col0 + i + k < valid) ? __uint_as_float(s[i + k]) : -INFINITY;
+    a = fmax3_nan(a, v[0], v[1]);
+    b = fmax3_nan(b, v[2], v[3]);
+  }
+  return fmax3_nan(a, b, -INFINITY);
+}
+
+// p = 2^(s scale - m) of 32 scores as 16 bf16 pairs at taddr; adds them to sum.
+// One pair in four takes the FMA-pipe exponential, the rest the MUFU.
+template <bool kFull>
+__device__ __forceinline__ void scores_exp32(const uint32_t (&s)[32], uint32_t taddr, int col0, int valid, float scale,
+                                             float neg_m, float (&sum)[4]) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float x0, x1, p0, p1;
+    ffma2(x0, x1, __uint_as_float(s[i]), __uint_as_float(s[i + 1]), scale, scale, neg_m, neg_m);
+    if (((i >> 1) & 3) == 3) {
+      exp2_poly4(p0, p1, x0, x1);
+    } else {
+      p0 = ex2_approx(x0);
+      p1 = ex2_approx(x1);
+    }
+    if (!kFull) {
+      p0 = col0 + i < valid ? p0 : 0.f;
+      p1 = col0 + i + 1 < valid ? p1 : 0.f;
+    }
+    if ((i >> 1) & 1)
+      fadd2(sum[2], sum[3], sum[2], sum[3], p0, p1);
+    else
+      fadd2(sum[0], sum[1], sum[0], sum[1], p0, p1);
+    pk[i >> 1] = pack_bf162(p0, p1);
+  }
+  tmem_st16(taddr, pk);
+}
+
+// One value of a cached row as f32.
+template <bool kE4m3>
+__device__ __forceinline__ float4 cached4(const uint8_t* pages, const uint8_t* scales, long long row, int lane) {
+  if (kE4m3) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(pages + row * 128)[lane];
+    const float s = e8m0_value(scales[row]);
+    const uint32_t lo = e4m3x2_f16x2(w), hi = e4m3x2_f16x2(w >> 16);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+  }
+  const uint2 w = reinterpret_cast<const uint2*>(pages + row * 256)[lane];
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+// The sum over keys [key0, limit) of 2^(score - m) V for one query row, by one
+// warp, lane holding dims 4 lane..: for a row whose tensor-core sum met an
+// infinity or NaN in a value that the row does not see (weight zero times
+// infinity). Slow, and only ever run on such values.
+template <bool kE4m3>
+__device__ __noinline__ float4 row_sum_seen(const PagedAttnParams& p, const int* pages, int head, const uint2* q_row, int key0,
+                                            int limit, float m) {
+  const int lane = lane_id();
+  const uint2 w = q_row[lane];
+  const float4 q = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int key = key0; key < limit; ++key) {
+    const long long row = ((static_cast<long long>(pages[key >> p.page_shift]) * p.Hkv + head) << p.page_shift) +
+                          (key & ((1 << p.page_shift) - 1));
+    const float4 k = cached4<kE4m3>(p.pool.k, p.pool.ks, row, lane);
+    float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float e = ex2_approx(fmaf(s, p.scale_log2, -m));
+    const float4 v = cached4<kE4m3>(p.pool.v, p.pool.vs, row, lane);
+    acc.x = fmaf(e, v.x, acc.x);
+    acc.y = fmaf(e, v.y, acc.y);
+    acc.z = fmaf(e, v.z, acc.z);
+    acc.w = fmaf(e, v.w, acc.w);
+  }
+  return acc;
+}
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const __grid_constant__ PagedTileParams tp) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const PagedAttnParams& p = tp.a;
+  constexpr uint32_t T32 = TileSmem::kTile;
+  uint8_t* sQ = smem + TileSmem::kQ;
+  uint8_t* sK = smem + TileSmem::kK;
+  uint8_t* sV = smem + TileSmem::kV;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + TileSmem::kBar);
+  uint64_t* q_full = bars + 0;    // [2] query tiles
+  uint64_t* k_full = bars + 2;    // [2] ring stages
+  uint64_t* k_empty = bars + 4;   // [2]
+  uint64_t* v_full = bars + 6;    // [2]
+  uint64_t* v_empty = bars + 8;   // [2]
+  uint64_t* s_full = bars + 10;   // [2] query tiles
+  uint64_t* p_full = bars + 12;   // [2 tiles][2 halves of the keys]
+  uint64_t* o_full = bars + 16;   // [2]
+  uint64_t* v_raw = bars + 18;    // values of a tile whose tail is still to be cleared
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* last_flag = tmem_slot + 2;
+
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&k_full[i], kE4m3 ? 128 : 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], kE4m3 ? 128 : 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[2 * i], 128);
+      mbar_init(&p_full[2 * i + 1], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(v_raw, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_launch();
+  grid_dep_wait();
+  const WaitGuard wg{abort_flag, p.status};
+  const int u_begin = p.cta_unit0[blockIdx.x], u_end = p.cta_unit0[blockIdx.x + 1];
+
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ producers
+    regs_down<64>();
+    int it = 0;       // key tiles so far, over all units
+    int tails = 0;
+    const int u_stop = kE4m3 || warp == 8 ? u_end : u_begin;
+    for (int u = u_begin; u < u_stop; ++u) {
+      const PagedUnit un = p.units[u];
+      const int* pages = p.pages + p.seq_page0[un.seq];
+      for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
+        const int s = it & 1;
+        const uint32_t ph = (it >> 1) & 1;
+        const int live = min(kTileKeys, un.key1 - key);  // keys of the tile that the unit uses
+        if constexpr (!kE4m3) {
+          const int ps = 1 << p.page_shift;
+          const int n_pages = (live + ps - 1) >> p.page_shift;
+          const bool tail = live < kTileKeys;
+          const uint32_t bytes = static_cast<uint32_t>(n_pages) << (p.page_shift + 8);
+          int row = 0;  // lane i: first pool row of the tile's page i
+          if (lane < n_pages) row = (pages[(key >> p.page_shift) + lane] * p.Hkv + un.head) << p.page_shift;
+          if (lane == 0) {
+            mbar_wait(&k_empty[s], ph ^ 1u, wg);
+            mbar_expect_tx(&k_full[s], bytes);
+          }
+          __syncwarp();
+          if (lane < n_pages) {
+            uint8_t* dst = sK + s * T32 + lane * (ps * 128);
+            tma_load_2d(dst, &tp.k_map, &k_full[s], 0, row);
+            tma_load_2d(dst + 16384, &tp.k_map, &k_full[s], 64, row);
+          }
+          uint64_t* vb = tail ? v_raw : &v_full[s];
+          if (lane == 0) {
+            mbar_wait(&v_empty[s], ph ^ 1u, wg);
+            mbar_expect_tx(vb, bytes);
+          }
+          __syncwarp();
+          if (lane < n_pages) {
+            uint8_t* dst = sV + s * T32 + lane * (ps * 128);
+            tma_load_2d(dst, &tp.v_map, vb, 0, row);
+            tma_load_2d(dst + 16384, &tp.v_map, vb, 64, row);
+          }
+          if (tail) {
+            // what lies behind the last key must not reach the sum, whatever it is: zero values
+            mbar_wait(v_raw, tails & 1, wg);
+            ++tails;
+            for (int i = lane; i < (kTileKeys - live) * 16; i += 32)
+              *reinterpret_cast<uint4*>(sV + s * T32 + tile_offset(live + (i >> 4), i & 15)) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_full[s]);
+          }
+        } else {
+          // eight lanes a row, 16 rows at a time over the four warps (a page holds whole runs of 16)
+          const int pt = threadIdx.x - 8 * 32, sub = pt >> 3, e = pt & 7;
+          const int page_mask = (1 << p.page_shift) - 1;
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint8_t* src = kv ? p.pool.v : p.pool.k;
+            const uint8_t* sc = kv ? p.pool.vs : p.pool.ks;
+            uint4 x[8];
+            uint32_t b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 16 * i + sub;
+              x[i] = make_uint4(0, 0, 0, 0);
+              b[i] = 127u;
+              if (r < live) {
+                const long long row = ((static_cast<long long>(pages[(key + 16 * i) >> p.page_shift]) * p.Hkv + un.head) << p.page_shift) +
+                                      ((key + r) & page_mask);
+                x[i] = __ldg(reinterpret_cast<const uint4*>(src + row * 128) + e);
+                b[i] = __ldg(sc + row);
+              }
+            }
+            mbar_wait(kv ? &v_empty[s] : &k_empty[s], ph ^ 1u, wg);
+            uint8_t* dst = (kv ? sV : sK) + s * T32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 16 * i + sub;
+              const E4m3Scale f(b[i]);
+              const uint2 w0 = e4m3x4_bf16(x[i].x, f), w1 = e4m3x4_bf16(x[i].y, f), w2 = e4m3x4_bf16(x[i].z, f), w3 = e4m3x4_bf16(x[i].w, f);
+              const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+              // lanes of the second box store their odd piece first: the eight lanes of a row then hit all banks once
+              const bool odd = e >= 4;
+              *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 1 : 0))) = odd ? hi : lo;
+              *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 0 : 1))) = odd ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(kv ? &v_full[s] : &k_full[s]);
+          }
+        }
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ MMA issue
+    regs_down<64>();
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_f16(128, 128, true, true, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(128, 128, true, true, false, true);
+      int it = 0, n_unit[2] = {0, 0}, n_p[2] = {0, 0};  // key tiles; units and key tiles per query tile
+      auto issue_s = [&](int t, int stage) {
+        const uint32_t ka = smem_u32(sK + stage * T32), qa = smem_u32(sQ + t * T32);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ss(tmem + t * 128u, kmajor_desc(qa, kk, 16384), kmajor_desc(ka, kk, 16384), idesc_qk, kk > 0);
+        umma_commit(&s_full[t]);
+      };
+      for (int u = u_begin; u < u_end; ++u) {
+        const PagedUnit un = p.units[u];
+        const int rows = (p.seq_q0[un.seq + 1] - p.seq_q0[un.seq]) * p.group - un.row0;
+        const int nt = rows > 128 ? 2 : 1;
+        const int tiles = (un.key1 - un.key0 + kTileKeys - 1) / kTileKeys;
+        for (int j = 0; j < tiles; ++j, ++it) {
+          const int s = it & 1;
+          const uint32_t ph = (it >> 1) & 1;
+          if (j == 0) {
+            mbar_wait(&k_full[s], ph, wg);
+            for (int t = 0; t < nt; ++t) {
+              mbar_wait(&q_full[t], n_unit[t] & 1, wg);
+              ++n_unit[t];
+              tc_fence_after();
+              issue_s(t, s);
+            }
+            umma_commit(&k_empty[s]);
+          }
+          const bool more = j + 1 < tiles;
+          const int s1 = (it + 1) & 1;
+          mbar_wait(&v_full[s], ph, wg);
+          const uint32_t va = smem_u32(sV + s * T32);
+          for (int t = 0; t < nt; ++t) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              mbar_wait(&p_full[2 * t + half], n_p[t] & 1, wg);
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                umma_ts(tmem + 256u + t * 128u, tmem + t * 128u + kk * 8u, mnmajor_desc(va, kk, 16384), idesc_pv,
+                        (j | kk) != 0);
+            }
+            ++n_p[t];
+            if (!more) umma_commit(&o_full[t]);
+            if (t == nt - 1) umma_commit(&v_empty[s]);
+            if (more) {
+              if (t == 0) {
+                mbar_wait(&k_full[s1], ((it + 1) >> 1) & 1, wg);
+                tc_fence_after();
+              }
+              issue_s(t, s1);  // overwrites P_t only after the P V MMAs above (in-order issue)
+              if (t == nt - 1) umma_commit(&k_empty[s1]);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax, one thread per query row
+    regs_up<192>();
+    const int t = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + t * 128u + lane_off;
+    const uint32_t tO = tmem + 256u + t * 128u + lane_off;
+    int n_s = 0, n_unit = 0;
+    for (int u = u_begin; u < u_end; ++u) {
+      const PagedUnit un = p.units[u];
+      const int q0 = p.seq_q0[un.seq], q_len = p.seq_q0[un.seq + 1] - q0;
+      const int unit_rows = min(kTileRows, q_len * p.group - un.row0);
+      if (t * 128 >= unit_rows) continue;
+      const int past = p.seq_kv[un.seq] - q_len, vis = p.seq_vis[un.seq];
+      auto out_row_of = [&](int r) {  // row of [T, Hq] of the unit's row r
+        const int rr = un.row0 + r;
+        return static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
+      };
+      // 16 lanes a row, two rows at a time
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = (warp & 3) * 32 + 2 * i + (lane >> 4);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (t * 128 + r < unit_rows) w = __ldg(p.q + out_row_of(t * 128 + r) * 16 + (lane & 15));
+        *reinterpret_cast<uint4*>(sQ + t * T32 + tile_offset(r, lane & 15)) = w;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[t]);
+      const bool live = t * 128 + row < unit_rows;
+      const int limit = max(vis, past + (un.row0 + min(t * 128 + row, unit_rows - 1)) / p.group + 1);
+      float m_run = -INFINITY, l_run = 0.f;
+      bool first = true;
+      for (int key = un.key0; key < un.key1; key += kTileKeys, ++n_s) {
+        mbar_wait(&s_full[t], n_s & 1, wg);
+        tc_fence_after();
+        const int valid = limit - key;  // keys of this tile that this row sees
+        // warp-uniform, as the tcgen05 instructions in the branches are
+        const bool full = __all_sync(0xffffffffu, valid >= kTileKeys);
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+        tmem_ld_wait();
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mx = full ? scores_max32<true>(s[c], mx, c * 32, valid) : scores_max32<false>(s[c], mx, c * 32, valid);
+        float m_tile = mx * p.scale_log2;
+        if (m_tile == INFINITY) m_tile = NAN;  // infinite scores have no softmax
+        // raised by -inf -> finite, by more than 2^8, and for good by a NaN
+        const bool need = !(m_tile <= m_run + kLazyRescaleLog2);
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_new = need ? m_tile : m_run;
+          const float alpha = need ? ex2_approx(m_run - m_new) : 1.f;
+          m_run = m_new;
+          if (!first) {
+            // S of this tile was issued after the previous P V, which is therefore complete
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t r[16];
+              tmem_ld16(tO + c * 16, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st16(tO + c * 16, r);
+            }
+            l_run *= alpha;
+          }
+        }
+        first = false;
+        const float neg_m = -finite_or_zero(m_run);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int c = 2 * half; c < 2 * half + 2; ++c) {
+            if (full)
+              scores_exp32<true>(s[c], tS + c * 16, c * 32, valid, p.scale_log2, neg_m, sum);
+            else
+              scores_exp32<false>(s[c], tS + c * 16, c * 32, valid, p.scale_log2, neg_m, sum);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * t + half]);
+        }
+        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      mbar_wait(&o_full[t], n_unit & 1, wg);
+      ++n_unit;
+      tc_fence_after();
+      const int nsplit = un.split >> 16, split = un.split & 0xffff;
+      const float inv = nsplit == 1 ? 1.0f / l_run : 1.0f;
+      const long long orow = out_row_of(min(t * 128 + row, unit_rows - 1));
+      float* slot = p.part + static_cast<long long>(un.slot0 + split) * kTileSlot;
+      float probe = 0.f;  // NaN if any sum is not finite
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tO + c * 32, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) probe = fmaf(__uint_as_float(r[i]), 0.f, probe);
+        if (live && nsplit == 1) {
+          uint4* dst = p.o + orow * 16 + c * 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(r[8 * i + k]) * inv;
+            dst[i] = pack_bf16x8(f);
+          }
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(slot + (t * 128 + row) * 128 + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        }
+        __syncwarp();
+      }
+      if (live) {
+        if (nsplit > 1)
+          reinterpret_cast<float2*>(slot + kTileRows * 128)[t * 128 + row] = make_float2(m_run, l_run);
+        else if (p.lse)
+          p.lse[orow] = lse_of(m_run, l_run);
+      }
+      // rows whose scores are fine but whose sum is not, behind keys they do not see
+      unsigned redo = __ballot_sync(0xffffffffu, live && !(probe == 0.f) && l_run < INFINITY && limit < un.key1);
+      while (redo) {
+        const int src = __ffs(redo) - 1;
+        redo &= redo - 1;
+        const int lim = __shfl_sync(0xffffffffu, limit, src);
+        const float m = finite_or_zero(__shfl_sync(0xffffffffu, m_run, src)), f = __shfl_sync(0xffffffffu, inv, src);
+        const int r = t * 128 + (warp & 3) * 32 + src;
+        const long long out_row = out_row_of(r);
+        const float4 acc = row_sum_seen<kE4m3>(p, p.pages + p.seq_page0[un.seq], un.head, reinterpret_cast<const uint2*>(p.q + out_row * 16),
+                                               un.key0, lim, m);
+        __syncwarp();  // the row as its thread wrote it; only what is not finite is replaced
+        if (nsplit == 1) {
+          uint2* dst = reinterpret_cast<uint2*>(p.o + out_row * 16) + lane;
+          uint2 w = *dst;
+          if ((w.x & 0x7f80u) == 0x7f80u) w.x = (w.x & 0xffff0000u) | (pack_bf162(acc.x * f, 0.f) & 0xffffu);
+          if ((w.x & 0x7f800000u) == 0x7f800000u) w.x = (w.x & 0xffffu) | (pack_bf162(0.f, acc.y * f) & 0xffff0000u);
+          if ((w.y & 0x7f80u) == 0x7f80u) w.y = (w.y & 0xffff0000u) | (pack_bf162(acc.z * f, 0.f) & 0xffffu);
+          if ((w.y & 0x7f800000u) == 0x7f800000u) w.y = (w.y & 0xffffu) | (pack_bf162(0.f, acc.w * f) & 0xffff0000u);
+          *dst = w;
+        } else {
+          float4* dst = reinterpret_cast<float4*>(slot + r * 128) + lane;
+          float4 w = *dst;
+          if (!isfinite(w.x)) w.x = acc.x;
+          if (!isfinite(w.y)) w.y = acc.y;
+          if (!isfinite(w.z)) w.z = acc.z;
+          if (!isfinite(w.w)) w.w = acc.w;
+          *dst = w;
+        }
+      }
+      if (nsplit > 1) {
+        // the last range to arrive merges all, in the order of the ranges
+        const int threads = unit_rows > 128 ? 256 : 128;
+        __threadfence();
+        named_bar_sync(1, threads);
+        if (threadIdx.x == 0) {
+          *last_flag = atomicInc(reinterpret_cast<unsigned*>(p.counters) + un.counter, nsplit - 1) == nsplit - 1;
+          __threadfence();
+        }
+        named_bar_sync(1, threads);
+        const bool last = *last_flag != 0u;
+        named_bar_sync(1, threads);  // read by all before the next unit may write it
+        if (last) {
+          const float* slots = p.part + static_cast<long long>(un.slot0) * kTileSlot;
+          for (int r = warp; r < unit_rows; r += threads / 32) {
+            float m = -INFINITY;
+            for (int i = 0; i < nsplit; ++i)
+              m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(slots + static_cast<long long>(i) * kTileSlot + kTileRows * 128) + r).x);
+            const float m0 = finite_or_zero(m);
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < nsplit; ++i) {
+              const float* sl = slots + static_cast<long long>(i) * kTileSlot;
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(sl + kTileRows * 128) + r);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + r * 128) + lane);
+              const float w = ex2_approx(ml.x - m0);
+              l = fmaf(ml.y, w, l);
+              acc.x = fmaf(v.x, w, acc.x);
+              acc.y = fmaf(v.y, w, acc.y);
+              acc.z = fmaf(v.z, w, acc.z);
+              acc.w = fmaf(v.w, w, acc.w);
+            }
+            const float f = 1.0f / l;
+            const long long out_row = out_row_of(r);
+            reinterpret_cast<uint2*>(p.o + out_row * 16)[lane] = make_uint2(pack_bf162(acc.x * f, acc.y * f), pack_bf162(acc.z * f, acc.w * f));
+            if (p.lse && lane == 0) p.lse[out_row] = lse_of(m, l);
+          }
+        }
+      }
+      tc_fence_before();  // the next unit's MMAs overwrite O after this thread's q_full arrival
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace mot
