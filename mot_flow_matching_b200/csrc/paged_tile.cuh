@@ -77,6 +77,16 @@ __device__ __forceinline__ void exp2_poly4(float& p0, float& p1, float x0, float
   p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
+// One lane of a converged warp. The MMA warp runs its loop with all lanes and
+// lets the elected one issue: under `if (lane == 0)` the compiler cannot keep
+// descriptors in uniform registers, and each tcgen05.mma then took 110 clocks to
+// issue, more than the 64 it takes to run.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0u;
+}
+
 // Byte offset of 16-byte piece `piece` (0..15) of row `row` in a 128 x 128 bf16
 // tile: two boxes of 64 dims, 128 bytes a row, pieces permuted by row & 7.
 __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
@@ -348,16 +358,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   } else if (warp >= 12) {
     // ------------------------------------------------------------ MMA issue
     regs_down<64>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, true, true, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(128, 128, true, true, false, true);
+      const bool leader = elect_one();
       int it = 0, n_unit[2] = {0, 0}, n_p[2] = {0, 0};  // key tiles; units and key tiles per query tile
+      const uint64_t q_desc = kmajor_desc(smem_u32(sQ), 0, 16384), k_desc = kmajor_desc(smem_u32(sK), 0, 16384);
+      const uint64_t v_desc = mnmajor_desc(smem_u32(sV), 0, 16384);
       auto issue_s = [&](int t, int stage) {
-        const uint32_t ka = smem_u32(sK + stage * T32), qa = smem_u32(sQ + t * T32);
+        const uint64_t qd = q_desc + t * (T32 >> 4), kd = k_desc + stage * (T32 >> 4);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ss(tmem + t * 128u, kmajor_desc(qa, kk, 16384), kmajor_desc(ka, kk, 16384), idesc_qk, kk > 0);
-        umma_commit(&s_full[t]);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t step = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            umma_ss(tmem + t * 128u, qd + step, kd + step, idesc_qk, kk > 0);
+          }
+          umma_commit(&s_full[t]);
+        }
       };
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
@@ -373,34 +390,38 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               mbar_wait(&q_full[t], n_unit[t] & 1, wg);
               ++n_unit[t];
               tc_fence_after();
+              __syncwarp();
               issue_s(t, s);
             }
-            umma_commit(&k_empty[s]);
+            if (leader) umma_commit(&k_empty[s]);
           }
           const bool more = j + 1 < tiles;
           const int s1 = (it + 1) & 1;
           mbar_wait(&v_full[s], ph, wg);
-          const uint32_t va = smem_u32(sV + s * T32);
+          const uint64_t vd = v_desc + s * (T32 >> 4);
           for (int t = 0; t < nt; ++t) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               mbar_wait(&p_full[2 * t + half], n_p[t] & 1, wg);
               tc_fence_after();
+              __syncwarp();
+              if (leader) {
 #pragma unroll
-              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                umma_ts(tmem + 256u + t * 128u, tmem + t * 128u + kk * 8u, mnmajor_desc(va, kk, 16384), idesc_pv,
-                        (j | kk) != 0);
+                for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                  umma_ts(tmem + 256u + t * 128u, tmem + t * 128u + kk * 8u, vd + kk * 128u, idesc_pv, (j | kk) != 0);
+              }
             }
             ++n_p[t];
-            if (!more) umma_commit(&o_full[t]);
-            if (t == nt - 1) umma_commit(&v_empty[s]);
+            if (leader && !more) umma_commit(&o_full[t]);
+            if (leader && t == nt - 1) umma_commit(&v_empty[s]);
             if (more) {
               if (t == 0) {
                 mbar_wait(&k_full[s1], ((it + 1) >> 1) & 1, wg);
                 tc_fence_after();
+                __syncwarp();
               }
               issue_s(t, s1);  // overwrites P_t only after the P V MMAs above (in-order issue)
-              if (t == nt - 1) umma_commit(&k_empty[s1]);
+              if (leader && t == nt - 1) umma_commit(&k_empty[s1]);
             }
           }
         }
@@ -426,12 +447,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         return static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
       };
       // 16 lanes a row, two rows at a time
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int r = (warp & 3) * 32 + 2 * i + (lane >> 4);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (t * 128 + r < unit_rows) w = __ldg(p.q + out_row_of(t * 128 + r) * 16 + (lane & 15));
-        *reinterpret_cast<uint4*>(sQ + t * T32 + tile_offset(r, lane & 15)) = w;
+      {
+        uint4 w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = (warp & 3) * 32 + 2 * i + (lane >> 4);
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (t * 128 + r < unit_rows) w[i] = __ldg(p.q + out_row_of(t * 128 + r) * 16 + (lane & 15));
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<uint4*>(sQ + t * T32 + tile_offset((warp & 3) * 32 + 2 * i + (lane >> 4), lane & 15)) = w[i];
       }
       fence_proxy_async_smem();
       mbar_arrive(&q_full[t]);
@@ -573,30 +599,54 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         const bool last = *last_flag != 0u;
         named_bar_sync(1, threads);  // read by all before the next unit may write it
         if (last) {
+          // a warp takes 32 rows: lane i the max and sum of row i, then eight rows' sums at a time, the loads of
+          // a range issued together
           const float* slots = p.part + static_cast<long long>(un.slot0) * kTileSlot;
-          for (int r = warp; r < unit_rows; r += threads / 32) {
-            float m = -INFINITY;
-            for (int i = 0; i < nsplit; ++i)
-              m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(slots + static_cast<long long>(i) * kTileSlot + kTileRows * 128) + r).x);
+          for (int r0 = warp * 32; r0 < unit_rows; r0 += threads) {
+            auto ml_of = [&](int i) {
+              return __ldcg(reinterpret_cast<const float2*>(slots + static_cast<long long>(i) * kTileSlot + kTileRows * 128) + r0 + lane);
+            };
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < nsplit; ++i) m = fmaxf(m, ml_of(i).x);
             const float m0 = finite_or_zero(m);
-            float l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
             for (int i = 0; i < nsplit; ++i) {
-              const float* sl = slots + static_cast<long long>(i) * kTileSlot;
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(sl + kTileRows * 128) + r);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + r * 128) + lane);
-              const float w = ex2_approx(ml.x - m0);
-              l = fmaf(ml.y, w, l);
-              acc.x = fmaf(v.x, w, acc.x);
-              acc.y = fmaf(v.y, w, acc.y);
-              acc.z = fmaf(v.z, w, acc.z);
-              acc.w = fmaf(v.w, w, acc.w);
+              const float2 ml = ml_of(i);
+              l = fmaf(ml.y, ex2_approx(ml.x - m0), l);
             }
             const float f = 1.0f / l;
-            const long long out_row = out_row_of(r);
-            reinterpret_cast<uint2*>(p.o + out_row * 16)[lane] = make_uint2(pack_bf162(acc.x * f, acc.y * f), pack_bf162(acc.z * f, acc.w * f));
-            if (p.lse && lane == 0) p.lse[out_row] = lse_of(m, l);
+            const long long my_row = out_row_of(min(r0 + lane, unit_rows - 1));
+            if (p.lse && r0 + lane < unit_rows) p.lse[my_row] = lse_of(m, l);
+            for (int rb = 0; rb < 32 && r0 + rb < unit_rows; rb += 8) {
+              float4 acc[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+              for (int i = 0; i < nsplit; ++i) {
+                const float4* src = reinterpret_cast<const float4*>(slots + static_cast<long long>(i) * kTileSlot + (r0 + rb) * 128) + lane;
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + k * 32);
+                const float wi = ex2_approx(ml_of(i).x - m0);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float w = __shfl_sync(0xffffffffu, wi, rb + k);
+                  acc[k].x = fmaf(v[k].x, w, acc[k].x);
+                  acc[k].y = fmaf(v[k].y, w, acc[k].y);
+                  acc[k].z = fmaf(v[k].z, w, acc[k].z);
+                  acc[k].w = fmaf(v[k].w, w, acc[k].w);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, rb + k);
+                const long long row_k = __shfl_sync(0xffffffffu, my_row, rb + k);
+                if (r0 + rb + k < unit_rows)
+                  reinterpret_cast<uint2*>(p.o + row_k * 16)[lane] =
+                      make_uint2(pack_bf162(acc[k].x * fk, acc[k].y * fk), pack_bf162(acc[k].z * fk, acc[k].w * fk));
+              }
+            }
           }
         }
       }
