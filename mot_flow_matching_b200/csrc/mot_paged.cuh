@@ -224,6 +224,15 @@ PagedPool pool_view(const mot_paged_pool* p) {
                    static_cast<uint8_t*>(p->v_scale)};
 }
 
+// rows of 128 bytes, box of `box_rows` rows, as they are
+bool map_bytes(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {128, rows}, strides[1] = {128};
+  const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
+  return encode_ready() && g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 mot_status paged_copy(mot_paged_t h, mot_paged_batch_t bt, void* k, void* v, int32_t rows, const mot_paged_pool* pool,
                       bool store, cudaStream_t st) {
   if (rows < bt->kv_max || (store && bt->repeated)) return MOT_ERR_INVALID_ARGUMENT;
@@ -267,7 +276,7 @@ mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights
   h->cfg = *cfg;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cfg->kv_dtype == MOT_PAGED_E4M3;
-  set_smem_attr(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, TileSmem::kBytes);
+  set_smem_attr(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, TileSmem::bytes(e4m3));
   int per_sm = 0;
   bool ok = cudaGetDevice(&h->device) == cudaSuccess &&
             cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) == cudaSuccess &&
@@ -559,11 +568,18 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
                      dim3(kSmallWarps * 32), 0, st, p);
     } else {
       const uint64_t rows = static_cast<uint64_t>(pool->n_pages) * c.n_kv_heads * c.page_size;
-      if (!e4m3 && (!map2d(&tp.k_map, pool->k, true, 128, rows, 128, c.page_size) ||
-                    !map2d(&tp.v_map, pool->v, true, 128, rows, 128, c.page_size)))
+      if (e4m3 ? !map_bytes(&tp.k_map, pool->k, rows, c.page_size) || !map_bytes(&tp.v_map, pool->v, rows, c.page_size)
+               : !map2d(&tp.k_map, pool->k, true, 128, rows, 128, c.page_size) ||
+                     !map2d(&tp.v_map, pool->v, true, 128, rows, 128, c.page_size))
         return MOT_ERR_CUDA;
+      // a tile's 128 rows are whole tokens where the group divides 128: one box
+      tp.q_tma = 128 % p.group == 0;
+      const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(c.n_q_heads), static_cast<cuuint64_t>(bt->tokens)};
+      const cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(c.n_q_heads) * 256};
+      const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(128 / p.group)};
+      if (tp.q_tma && !encode(&tp.q_map, q, true, 3, dims, strides, box)) return MOT_ERR_CUDA;
       e = launch_pdl(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, dim3(h->ctas[1]),
-                     dim3(kTileThreads), TileSmem::kBytes, st, tp);
+                     dim3(kTileThreads), TileSmem::bytes(e4m3), st, tp);
     }
   }
   return e == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;

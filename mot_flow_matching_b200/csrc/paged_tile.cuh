@@ -10,11 +10,13 @@
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, one thread per query row with its
 // 128 scores in registers, so that the running max and sum need no exchange.
-// Warps 8-11: producers; bf16 pages: one TMA box per page and 64 dims (128-byte
-// swizzle, which is why page_size is a multiple of the 8-row swizzle atom),
-// issued by warp 8; e4m3 pages: 16-byte loads, each value times its row's power
-// of two into bf16 (exact) and into the same swizzled tile, so that everything
-// behind the producers is one code. Warp 12: MMA issue. The registers are split
+// Warp 12: MMA issue; warp 13: the query tiles, loaded while the unit before
+// still runs; warp 14: the pages. bf16 pages: one TMA box per page and 64 dims
+// (128-byte swizzle, which is why page_size is a multiple of the 8-row swizzle
+// atom) straight into the operand tiles. e4m3 pages: boxes of raw rows and their
+// scales into a staging tile each for keys and values, from which warps 8-11 put
+// each value times its row's power of two into bf16 (exact) and into the same
+// swizzled tiles, so that everything behind is one code. The registers are split
 // by setmaxnreg: 2 x 192 + 2 x 64 of the 4 x 128 a thread the block starts with.
 //
 // Probabilities are bf16, since they meet bf16 values in one MMA: half a step
@@ -32,7 +34,10 @@ constexpr int kTileKeys = 128;
 constexpr int kTileSlot = kTileRows * 128 + kTileRows * 2;  // floats of a partial
 
 struct PagedTileParams {
-  CUtensorMap k_map, v_map;  // bf16 pools: 2D {128, n_pages * Hkv * page_size}, box {64, page_size}
+  // 2D {128, n_pages * Hkv * page_size}; bf16: box {64, page_size}, 128-byte swizzle; e4m3: bytes, box {128, page_size}
+  CUtensorMap k_map, v_map;
+  CUtensorMap q_map;         // 3D {128, Hq, T}, box {64, group, 128 / group} (q_tma)
+  int q_tma;                 // the group is a power of two
   PagedAttnParams a;
 };
 
@@ -42,7 +47,10 @@ struct TileSmem {
   static constexpr uint32_t kK = kQ + 2 * kTile;
   static constexpr uint32_t kV = kK + 2 * kTile;
   static constexpr uint32_t kBar = kV + 2 * kTile;
-  static constexpr uint32_t kBytes = kBar + 256 + 1024;
+  static constexpr uint32_t kRaw = kBar + 512;  // e4m3: [keys, values] 128 rows of 128 bytes, then 2 x 128 scales
+  static constexpr uint32_t kRawTile = 16384;
+  static constexpr uint32_t kScale = kRaw + 2 * kRawTile;
+  static constexpr uint32_t bytes(bool e4m3) { return (e4m3 ? kScale + 256 : kRaw) + 1024; }
 };
 
 constexpr int kTileThreads = 512;
@@ -85,6 +93,13 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0u;
+}
+
+// untiled bulk copy: addresses and size multiples of 16 bytes
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // Byte offset of 16-byte piece `piece` (0..15) of row `row` in a 128 x 128 bf16
@@ -230,17 +245,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   uint64_t* p_full = bars + 12;   // [2 tiles][2 halves of the keys]
   uint64_t* o_full = bars + 16;   // [2]
   uint64_t* v_raw = bars + 18;    // values of a tile whose tail is still to be cleared
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  uint64_t* q_empty = bars + 19;  // [2]
+  uint64_t* raw_full = bars + 21;   // [2] keys, values (e4m3)
+  uint64_t* raw_empty = bars + 23;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* last_flag = tmem_slot + 2;
 
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 128);
-      mbar_init(&k_full[i], kE4m3 ? 128 : 1);
+      mbar_init(&q_full[i], 1);
+      mbar_init(&k_full[i], kE4m3 ? 4 : 1);
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], kE4m3 ? 128 : 1);
+      mbar_init(&v_full[i], kE4m3 ? 4 : 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[2 * i], 128);
@@ -248,6 +266,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       mbar_init(&o_full[i], 1);
     }
     mbar_init(v_raw, 1);
+    mbar_init(&q_empty[0], 1);
+    mbar_init(&q_empty[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -265,99 +289,156 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   const int u_begin = p.cta_unit0[blockIdx.x], u_end = p.cta_unit0[blockIdx.x + 1];
 
   if (warp >= 8 && warp < 12) {
-    // ------------------------------------------------------------ producers
     regs_down<64>();
-    int it = 0;       // key tiles so far, over all units
-    int tails = 0;
-    const int u_stop = kE4m3 || warp == 8 ? u_end : u_begin;
-    for (int u = u_begin; u < u_stop; ++u) {
-      const PagedUnit un = p.units[u];
-      const int* pages = p.pages + p.seq_page0[un.seq];
-      for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
-        const int s = it & 1;
-        const uint32_t ph = (it >> 1) & 1;
-        const int live = min(kTileKeys, un.key1 - key);  // keys of the tile that the unit uses
-        if constexpr (!kE4m3) {
-          const int ps = 1 << p.page_shift;
-          const int n_pages = (live + ps - 1) >> p.page_shift;
-          const bool tail = live < kTileKeys;
-          const uint32_t bytes = static_cast<uint32_t>(n_pages) << (p.page_shift + 8);
-          int row = 0;  // lane i: first pool row of the tile's page i
-          if (lane < n_pages) row = (pages[(key >> p.page_shift) + lane] * p.Hkv + un.head) << p.page_shift;
-          if (lane == 0) {
-            mbar_wait(&k_empty[s], ph ^ 1u, wg);
-            mbar_expect_tx(&k_full[s], bytes);
-          }
-          __syncwarp();
-          if (lane < n_pages) {
-            uint8_t* dst = sK + s * T32 + lane * (ps * 128);
-            tma_load_2d(dst, &tp.k_map, &k_full[s], 0, row);
-            tma_load_2d(dst + 16384, &tp.k_map, &k_full[s], 64, row);
-          }
-          uint64_t* vb = tail ? v_raw : &v_full[s];
-          if (lane == 0) {
-            mbar_wait(&v_empty[s], ph ^ 1u, wg);
-            mbar_expect_tx(vb, bytes);
-          }
-          __syncwarp();
-          if (lane < n_pages) {
-            uint8_t* dst = sV + s * T32 + lane * (ps * 128);
-            tma_load_2d(dst, &tp.v_map, vb, 0, row);
-            tma_load_2d(dst + 16384, &tp.v_map, vb, 64, row);
-          }
-          if (tail) {
-            // what lies behind the last key must not reach the sum, whatever it is: zero values
-            mbar_wait(v_raw, tails & 1, wg);
-            ++tails;
-            for (int i = lane; i < (kTileKeys - live) * 16; i += 32)
-              *reinterpret_cast<uint4*>(sV + s * T32 + tile_offset(live + (i >> 4), i & 15)) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_full[s]);
-          }
-        } else {
-          // eight lanes a row, 16 rows at a time over the four warps (a page holds whole runs of 16)
-          const int pt = threadIdx.x - 8 * 32, sub = pt >> 3, e = pt & 7;
-          const int page_mask = (1 << p.page_shift) - 1;
+    if constexpr (kE4m3) {
+      // ---------------------------------------------------------- e4m3 -> bf16 operand tiles
+      // eight lanes a row, four rows a warp at a time
+      const int ct = threadIdx.x - 8 * 32, sub = ct >> 3, e = ct & 7;
+      const bool odd = e >= 4;
+      int it = 0;
+      for (int u = u_begin; u < u_end; ++u) {
+        const PagedUnit un = p.units[u];
+        for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
+          const int s = it & 1;
+          const int live = min(kTileKeys, un.key1 - key);
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
-            const uint8_t* src = kv ? p.pool.v : p.pool.k;
-            const uint8_t* sc = kv ? p.pool.vs : p.pool.ks;
-            uint4 x[8];
-            uint32_t b[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = 16 * i + sub;
-              x[i] = make_uint4(0, 0, 0, 0);
-              b[i] = 127u;
-              if (r < live) {
-                const long long row = ((static_cast<long long>(pages[(key + 16 * i) >> p.page_shift]) * p.Hkv + un.head) << p.page_shift) +
-                                      ((key + r) & page_mask);
-                x[i] = __ldg(reinterpret_cast<const uint4*>(src + row * 128) + e);
-                b[i] = __ldg(sc + row);
-              }
-            }
-            mbar_wait(kv ? &v_empty[s] : &k_empty[s], ph ^ 1u, wg);
+            mbar_wait(&raw_full[kv], it & 1, wg);
+            mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((it >> 1) & 1) ^ 1u, wg);
+            const uint8_t* raw = smem + TileSmem::kRaw + kv * TileSmem::kRawTile;
+            const uint8_t* scale = smem + TileSmem::kScale + kv * 128;
             uint8_t* dst = (kv ? sV : sK) + s * T32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int r = 16 * i + sub;
-              const E4m3Scale f(b[i]);
-              const uint2 w0 = e4m3x4_bf16(x[i].x, f), w1 = e4m3x4_bf16(x[i].y, f), w2 = e4m3x4_bf16(x[i].z, f), w3 = e4m3x4_bf16(x[i].w, f);
+              uint4 x = make_uint4(0, 0, 0, 0);  // what lies behind the last key must not reach the sum, whatever it is
+              uint32_t b = 127u;
+              if (r < live) {
+                x = *reinterpret_cast<const uint4*>(raw + r * 128 + e * 16);
+                b = scale[r];
+              }
+              const E4m3Scale f(b);
+              const uint2 w0 = e4m3x4_bf16(x.x, f), w1 = e4m3x4_bf16(x.y, f), w2 = e4m3x4_bf16(x.z, f), w3 = e4m3x4_bf16(x.w, f);
               const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
               // lanes of the second box store their odd piece first: the eight lanes of a row then hit all banks once
-              const bool odd = e >= 4;
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 1 : 0))) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 0 : 1))) = odd ? lo : hi;
             }
             fence_proxy_async_smem();
-            mbar_arrive(kv ? &v_full[s] : &k_full[s]);
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(kv ? &v_full[s] : &k_full[s]);
+              mbar_arrive(&raw_empty[kv]);
+            }
           }
         }
       }
     }
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ MMA issue
     regs_down<64>();
+    if (warp == 13) {
+      // ---------------------------------------------------------- query tiles, a unit ahead
+      int n_unit[2] = {0, 0};
+      for (int u = u_begin; u < u_end; ++u) {
+        const PagedUnit un = p.units[u];
+        const int q0 = p.seq_q0[un.seq];
+        const int rows = min(kTileRows, (p.seq_q0[un.seq + 1] - q0) * p.group - un.row0);
+        for (int t = 0; t * 128 < rows; ++t) {
+          mbar_wait(&q_empty[t], (n_unit[t] & 1) ^ 1u, wg);
+          ++n_unit[t];
+          if (tp.q_tma) {
+            // 128 / group tokens of the group's heads are the tile's rows in order; rows behind the sequence's last
+            // are the next one's, or zero, and go nowhere
+            if (lane == 0) {
+              const int token = q0 + un.row0 / p.group + t * (128 / p.group);
+              mbar_expect_tx(&q_full[t], T32);
+              tma_load_3d(sQ + t * T32, &tp.q_map, &q_full[t], 0, un.head * p.group, token);
+              tma_load_3d(sQ + t * T32 + 16384, &tp.q_map, &q_full[t], 64, un.head * p.group, token);
+            }
+          } else {
+#pragma unroll 4
+            for (int i = lane; i < 128 * 16; i += 32) {
+              const int r = t * 128 + (i >> 4), rr = un.row0 + r;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (r < rows)
+                w = __ldg(p.q + (static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group) * 16 + (i & 15));
+              *reinterpret_cast<uint4*>(sQ + t * T32 + tile_offset(i >> 4, i & 15)) = w;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[t]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (warp == 14) {
+      // ---------------------------------------------------------- pages; lane i takes page i of a tile
+      const int ps = 1 << p.page_shift;
+      int it = 0, tails = 0;  // key tiles so far, over all units
+      for (int u = u_begin; u < u_end; ++u) {
+        const PagedUnit un = p.units[u];
+        const int* pages = p.pages + p.seq_page0[un.seq];
+        for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
+          const int s = it & 1;
+          const uint32_t ph = (it >> 1) & 1;
+          const int live = min(kTileKeys, un.key1 - key);  // keys of the tile that the unit uses
+          const int n_pages = (live + ps - 1) >> p.page_shift;
+          int row = 0;  // first pool row of the page
+          if (lane < n_pages) row = (pages[(key >> p.page_shift) + lane] * p.Hkv + un.head) << p.page_shift;
+          if constexpr (kE4m3) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              if (lane == 0) {
+                mbar_wait(&raw_empty[kv], (it & 1) ^ 1u, wg);
+                mbar_expect_tx(&raw_full[kv], static_cast<uint32_t>(n_pages * ps) * 129u);
+              }
+              __syncwarp();
+              if (lane < n_pages) {
+                tma_load_2d(smem + TileSmem::kRaw + kv * TileSmem::kRawTile + lane * ps * 128, kv ? &tp.v_map : &tp.k_map,
+                            &raw_full[kv], 0, row);
+                bulk_load(smem + TileSmem::kScale + kv * 128 + lane * ps, (kv ? p.pool.vs : p.pool.ks) + row, ps, &raw_full[kv]);
+              }
+            }
+          } else {
+            const bool tail = live < kTileKeys;
+            const uint32_t bytes = static_cast<uint32_t>(n_pages * ps) * 256u;
+            if (lane == 0) {
+              mbar_wait(&k_empty[s], ph ^ 1u, wg);
+              mbar_expect_tx(&k_full[s], bytes);
+            }
+            __syncwarp();
+            if (lane < n_pages) {
+              uint8_t* dst = sK + s * T32 + lane * (ps * 128);
+              tma_load_2d(dst, &tp.k_map, &k_full[s], 0, row);
+              tma_load_2d(dst + 16384, &tp.k_map, &k_full[s], 64, row);
+            }
+            uint64_t* vb = tail ? v_raw : &v_full[s];
+            if (lane == 0) {
+              mbar_wait(&v_empty[s], ph ^ 1u, wg);
+              mbar_expect_tx(vb, bytes);
+            }
+            __syncwarp();
+            if (lane < n_pages) {
+              uint8_t* dst = sV + s * T32 + lane * (ps * 128);
+              tma_load_2d(dst, &tp.v_map, vb, 0, row);
+              tma_load_2d(dst + 16384, &tp.v_map, vb, 64, row);
+            }
+            if (tail) {
+              // what lies behind the last key must not reach the sum, whatever it is: zero values
+              mbar_wait(v_raw, tails & 1, wg);
+              ++tails;
+              for (int i = lane; i < (kTileKeys - live) * 16; i += 32)
+                *reinterpret_cast<uint4*>(sV + s * T32 + tile_offset(live + (i >> 4), i & 15)) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&v_full[s]);
+            }
+          }
+        }
+      }
+    }
+    // ------------------------------------------------------------ MMA issue
     if (warp == 12) {
       constexpr uint32_t idesc_qk = idesc_f16(128, 128, true, true, false, false);
       constexpr uint32_t idesc_pv = idesc_f16(128, 128, true, true, false, true);
@@ -365,7 +446,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       int it = 0, n_unit[2] = {0, 0}, n_p[2] = {0, 0};  // key tiles; units and key tiles per query tile
       const uint64_t q_desc = kmajor_desc(smem_u32(sQ), 0, 16384), k_desc = kmajor_desc(smem_u32(sK), 0, 16384);
       const uint64_t v_desc = mnmajor_desc(smem_u32(sV), 0, 16384);
-      auto issue_s = [&](int t, int stage) {
+      auto issue_s = [&](int t, int stage, bool last) {
         const uint64_t qd = q_desc + t * (T32 >> 4), kd = k_desc + stage * (T32 >> 4);
         if (leader) {
 #pragma unroll
@@ -374,6 +455,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             umma_ss(tmem + t * 128u, qd + step, kd + step, idesc_qk, kk > 0);
           }
           umma_commit(&s_full[t]);
+          if (last) umma_commit(&q_empty[t]);
         }
       };
       for (int u = u_begin; u < u_end; ++u) {
@@ -391,7 +473,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               ++n_unit[t];
               tc_fence_after();
               __syncwarp();
-              issue_s(t, s);
+              issue_s(t, s, tiles == 1);
             }
             if (leader) umma_commit(&k_empty[s]);
           }
@@ -420,7 +502,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
                 tc_fence_after();
                 __syncwarp();
               }
-              issue_s(t, s1);  // overwrites P_t only after the P V MMAs above (in-order issue)
+              issue_s(t, s1, j + 2 == tiles);  // overwrites P_t only after the P V MMAs above (in-order issue)
               if (leader && t == nt - 1) umma_commit(&k_empty[s1]);
             }
           }
@@ -447,20 +529,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         return static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
       };
       // 16 lanes a row, two rows at a time
-      {
-        uint4 w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = (warp & 3) * 32 + 2 * i + (lane >> 4);
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (t * 128 + r < unit_rows) w[i] = __ldg(p.q + out_row_of(t * 128 + r) * 16 + (lane & 15));
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          *reinterpret_cast<uint4*>(sQ + t * T32 + tile_offset((warp & 3) * 32 + 2 * i + (lane >> 4), lane & 15)) = w[i];
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&q_full[t]);
       const bool live = t * 128 + row < unit_rows;
       const int limit = max(vis, past + (un.row0 + min(t * 128 + row, unit_rows - 1)) / p.group + 1);
       float m_run = -INFINITY, l_run = 0.f;
