@@ -108,33 +108,31 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
   return static_cast<uint32_t>((piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// Four e4m3 (bytes of w) times 2^(b - 127) as two bf16 pairs, exactly: the byte's
-// exponent and mantissa land in the bf16 fields 2^120 too small, subnormals
-// included, and one or two multiplications by powers of two put that right
-// (f2 = 1 but for scales whose first factor would leave the bf16 range).
-struct E4m3Scale {
-  __nv_bfloat162 f1, f2;
-  bool two;
-  __device__ __forceinline__ explicit E4m3Scale(uint32_t b) {
-    two = b > 134u && b != 255u;
-    const uint32_t e1 = b == 255u ? 0x7fffu : (two ? 254u << 7 : (b + 120u) << 7);
-    const uint32_t e2 = two ? (b - 7u) << 7 : 0x3f80u;
-    const uint32_t w1 = e1 | (e1 << 16), w2 = e2 | (e2 << 16);
-    f1 = *reinterpret_cast<const __nv_bfloat162*>(&w1);
-    f2 = *reinterpret_cast<const __nv_bfloat162*>(&w2);
-  }
-};
+// Sixteen e4m3 times 2^(b - 127) as bf16, exactly: a byte's exponent and mantissa
+// land in the bf16 fields 2^120 too small, subnormals included, and one
+// multiplication by a power of two puts that right. A scale whose factor would
+// leave the bf16 range (b > 134: rows with values past 2^16) takes a second one.
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t bits) { return bits | (bits << 16); }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-__device__ __forceinline__ uint2 e4m3x4_bf16(uint32_t w, const E4m3Scale& s) {
-  uint32_t r[2] = {__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424)};
+template <bool kTwo>
+__device__ __forceinline__ void e4m3x16_bf16(const uint4& x, uint32_t b, uint4& lo, uint4& hi) {
+  const bool two = kTwo && b > 134u && b != 255u;
+  const uint32_t f1 = bf16_pair(b == 255u ? 0x7fffu : two ? 254u << 7 : (b + 120u) << 7);
+  const uint32_t f2 = bf16_pair(two ? (b - 7u) << 7 : 0x3f80u);
+  uint32_t r[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    r[i] = ((r[i] & 0x7f007f00u) >> 4) | (r[i] & 0x80008000u);
-    __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[i]), s.f1);
-    if (s.two) v = __hmul2(v, s.f2);
-    r[i] = *reinterpret_cast<const uint32_t*>(&v);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
+    const uint32_t v = __byte_perm(w, 0u, (i & 1) ? 0x3424 : 0x1404);  // a byte on top of each half
+    r[i] = mul_bf16x2(((v & 0x7f007f00u) >> 4) | (v & 0x80008000u), f1);
+    if (kTwo) r[i] = mul_bf16x2(r[i], f2);
   }
-  return make_uint2(r[0], r[1]);
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
 // a row's score max over 32 columns from col0; columns at or behind `valid` masked; NaN comes out as NaN
@@ -308,21 +306,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             const uint8_t* raw = smem + TileSmem::kRaw + kv * TileSmem::kRawTile;
             const uint8_t* scale = smem + TileSmem::kScale + kv * 128;
             uint8_t* dst = (kv ? sV : sK) + s * T32;
+            uint32_t sc[8];
+            bool big = false;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int r = 16 * i + sub;
-              uint4 x = make_uint4(0, 0, 0, 0);  // what lies behind the last key must not reach the sum, whatever it is
-              uint32_t b = 127u;
-              if (r < live) {
-                x = *reinterpret_cast<const uint4*>(raw + r * 128 + e * 16);
-                b = scale[r];
-              }
-              const E4m3Scale f(b);
-              const uint2 w0 = e4m3x4_bf16(x.x, f), w1 = e4m3x4_bf16(x.y, f), w2 = e4m3x4_bf16(x.z, f), w3 = e4m3x4_bf16(x.w, f);
-              const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+              sc[i] = scale[16 * i + sub];
+              big |= sc[i] > 134u;
+            }
+            auto put = [&](int r, const uint4& lo, const uint4& hi) {
               // lanes of the second box store their odd piece first: the eight lanes of a row then hit all banks once
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 1 : 0))) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 0 : 1))) = odd ? lo : hi;
+            };
+            if (live == kTileKeys && !__any_sync(0xffffffffu, big)) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = 16 * i + sub;
+                uint4 lo, hi;
+                e4m3x16_bf16<false>(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), sc[i], lo, hi);
+                put(r, lo, hi);
+              }
+            } else {
+#pragma unroll 2
+              for (int i = 0; i < 8; ++i) {
+                const int r = 16 * i + sub;
+                uint4 lo, hi;
+                e4m3x16_bf16<true>(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], lo, hi);
+                // what lies behind the last key must not reach the sum, whatever it is
+                if (r >= live) lo = hi = make_uint4(0, 0, 0, 0);
+                put(r, lo, hi);
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
