@@ -34,6 +34,8 @@ struct PagedTables {
   int unit_cap[2];
 };
 
+static_assert(TileSmem::bytes(true) <= 232448, "shared memory");
+
 // Query rows (tokens times heads of the group) up to which a sequence goes to
 // the few-rows kernel.
 constexpr int kSmallMaxRows = 2 * kSmallRows;

@@ -14,14 +14,19 @@
 // still runs; warp 14: the pages. bf16 pages: one TMA box per page and 64 dims
 // (128-byte swizzle, which is why page_size is a multiple of the 8-row swizzle
 // atom) straight into the operand tiles. e4m3 pages: boxes of raw rows and their
-// scales into a staging tile each for keys and values, from which warps 8-11 put
-// each value times its row's power of two into bf16 (exact) and into the same
-// swizzled tiles, so that everything behind is one code. The registers are split
+// scales into a staging tile each for keys and values, from which warps 8-11
+// make f16 operand tiles: e4m3 -> f16 is one exact instruction per pair, and the
+// row's scale relative to the tile's largest is a power of two <= 1 (exact down
+// to 2^-15 of the largest; below that a value is off by at most 2^-25 of it). The
+// tile's largest scale goes into the scores (keys), and into the weights
+// relative to the largest so far (values), as one factor per tile; queries are
+// made f16 in place, each row scaled by a power of two that its thread puts back. The registers are split
 // by setmaxnreg: 2 x 192 + 2 x 64 of the 4 x 128 a thread the block starts with.
 //
-// Probabilities are bf16, since they meet bf16 values in one MMA: half a step
-// is 2^-9 on average below what the bf16 output itself loses; the row sum is
-// taken in f32 from the unrounded ones. The running max is raised, and O_t
+// Probabilities are of the values' type, since they meet them in one MMA: bf16
+// ones lose about what the bf16 output itself does (half a step, averaged over
+// the keys), f16 ones an eighth of that; the row sum is taken in f32 from the
+// unrounded ones. The running max is raised, and O_t
 // rescaled through TMEM, only when a row's max grows by more than 2^8.
 #pragma once
 
@@ -47,10 +52,12 @@ struct TileSmem {
   static constexpr uint32_t kK = kQ + 2 * kTile;
   static constexpr uint32_t kV = kK + 2 * kTile;
   static constexpr uint32_t kBar = kV + 2 * kTile;
-  static constexpr uint32_t kRaw = kBar + 512;  // e4m3: [keys, values] 128 rows of 128 bytes, then 2 x 128 scales
+  static constexpr uint32_t kRaw = kBar + 256;  // e4m3: [keys, values] 128 rows of 128 bytes, then 2 x 128 scales
   static constexpr uint32_t kRawTile = 16384;
   static constexpr uint32_t kScale = kRaw + 2 * kRawTile;
-  static constexpr uint32_t bytes(bool e4m3) { return (e4m3 ? kScale + 256 : kRaw) + 1024; }
+  static constexpr uint32_t kRef = kScale + 256;   // e4m3: largest scale bytes, keys [4 tiles], values [4 tiles]
+  static constexpr uint32_t kQScale = kRef + 64;   // e4m3: [2 units][256 rows] 127 + exponent of a query row's factor
+  static constexpr uint32_t bytes(bool e4m3) { return (e4m3 ? kQScale + 512 : kRaw) + 1024; }
 };
 
 constexpr int kTileThreads = 512;
@@ -108,28 +115,20 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
   return static_cast<uint32_t>((piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// Sixteen e4m3 times 2^(b - 127) as bf16, exactly: a byte's exponent and mantissa
-// land in the bf16 fields 2^120 too small, subnormals included, and one
-// multiplication by a power of two puts that right. A scale whose factor would
-// leave the bf16 range (b > 134: rows with values past 2^16) takes a second one.
-__device__ __forceinline__ uint32_t bf16_pair(uint32_t bits) { return bits | (bits << 16); }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-template <bool kTwo>
-__device__ __forceinline__ void e4m3x16_bf16(const uint4& x, uint32_t b, uint4& lo, uint4& hi) {
-  const bool two = kTwo && b > 134u && b != 255u;
-  const uint32_t f1 = bf16_pair(b == 255u ? 0x7fffu : two ? 254u << 7 : (b + 120u) << 7);
-  const uint32_t f2 = bf16_pair(two ? (b - 7u) << 7 : 0x3f80u);
+// Sixteen e4m3 times 2^(b - ref) as f16 (b <= ref, or b = 255: NaN).
+__device__ __forceinline__ void e4m3x16_f16(const uint4& x, uint32_t b, uint32_t ref, uint4& lo, uint4& hi) {
+  const int d = static_cast<int>(ref) - static_cast<int>(b);
+  uint32_t f = d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  if (b == 255u) f = 0x7e00u;
+  f |= f << 16;
+  const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
   uint32_t r[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
-    const uint32_t v = __byte_perm(w, 0u, (i & 1) ? 0x3424 : 0x1404);  // a byte on top of each half
-    r[i] = mul_bf16x2(((v & 0x7f007f00u) >> 4) | (v & 0x80008000u), f1);
-    if (kTwo) r[i] = mul_bf16x2(r[i], f2);
+    const uint32_t h = e4m3x2_f16x2(w >> (16 * (i & 1)));
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), f2);
+    r[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
@@ -150,9 +149,9 @@ __device__ __forceinline__ float scores_max32(const uint32_t (&s)[32], float m, 
   return fmax3_nan(a, b, -INFINITY);
 }
 
-// p = 2^(s scale - m) of 32 scores as 16 bf16 pairs at taddr; adds them to sum.
+// p = 2^(s scale - m) of 32 scores as 16 pairs (bf16 or f16) at taddr; adds them to sum.
 // One pair in four takes the FMA-pipe exponential, the rest the MUFU.
-template <bool kFull>
+template <bool kFull, bool kBf16>
 __device__ __forceinline__ void scores_exp32(const uint32_t (&s)[32], uint32_t taddr, int col0, int valid, float scale,
                                              float neg_m, float (&sum)[4]) {
   uint32_t pk[16];
@@ -174,7 +173,7 @@ __device__ __forceinline__ void scores_exp32(const uint32_t (&s)[32], uint32_t t
       fadd2(sum[2], sum[3], sum[2], sum[3], p0, p1);
     else
       fadd2(sum[0], sum[1], sum[0], sum[1], p0, p1);
-    pk[i >> 1] = pack_bf162(p0, p1);
+    pk[i >> 1] = kBf16 ? pack_bf162(p0, p1) : pack_half2(p0, p1);
   }
   tmem_st16(taddr, pk);
 }
@@ -246,14 +245,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   uint64_t* q_empty = bars + 19;  // [2]
   uint64_t* raw_full = bars + 21;   // [2] keys, values (e4m3)
   uint64_t* raw_empty = bars + 23;  // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+  uint64_t* q_raw = bars + 25;      // [2] query tiles before their conversion (e4m3)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* last_flag = tmem_slot + 2;
 
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
+      mbar_init(&q_full[i], kE4m3 ? 4 : 1);
       mbar_init(&k_full[i], kE4m3 ? 4 : 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], kE4m3 ? 4 : 1);
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     for (int i = 0; i < 2; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
+      mbar_init(&q_raw[i], 1);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -289,11 +290,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   if (warp >= 8 && warp < 12) {
     regs_down<64>();
     if constexpr (kE4m3) {
-      // ---------------------------------------------------------- e4m3 -> bf16 operand tiles
+      // ---------------------------------------------------------- e4m3 pages, bf16 queries -> f16 operand tiles
       // eight lanes a row, four rows a warp at a time
       const int ct = threadIdx.x - 8 * 32, sub = ct >> 3, e = ct & 7;
       const bool odd = e >= 4;
-      int it = 0;
+      volatile uint32_t* refs = reinterpret_cast<volatile uint32_t*>(smem + TileSmem::kRef);
+      uint8_t* q_scale = smem + TileSmem::kQScale;
+      int it = 0, n_unit[2] = {0, 0};
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
         for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
@@ -302,28 +305,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             mbar_wait(&raw_full[kv], it & 1, wg);
-            mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((it >> 1) & 1) ^ 1u, wg);
             const uint8_t* raw = smem + TileSmem::kRaw + kv * TileSmem::kRawTile;
             const uint8_t* scale = smem + TileSmem::kScale + kv * 128;
             uint8_t* dst = (kv ? sV : sK) + s * T32;
-            uint32_t sc[8];
-            bool big = false;
+            // the tile's largest scale: lane i looks at rows 4i..4i+3; NaN rows and those behind the last key do not count
+            uint32_t top = 0u;
+            {
+              const uint32_t w = reinterpret_cast<const uint32_t*>(scale)[lane];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              sc[i] = scale[16 * i + sub];
-              big |= sc[i] > 134u;
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t b = (w >> (8 * i)) & 255u;
+                if (4 * lane + i < live && b != 255u) top = max(top, b);
+              }
             }
+            const uint32_t ref = __reduce_max_sync(0xffffffffu, top);
+            mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((it >> 1) & 1) ^ 1u, wg);
+            if (ct == 0) refs[kv * 4 + (it & 3)] = ref;
             auto put = [&](int r, const uint4& lo, const uint4& hi) {
               // lanes of the second box store their odd piece first: the eight lanes of a row then hit all banks once
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 1 : 0))) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 0 : 1))) = odd ? lo : hi;
             };
-            if (live == kTileKeys && !__any_sync(0xffffffffu, big)) {
+            if (live == kTileKeys) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const int r = 16 * i + sub;
                 uint4 lo, hi;
-                e4m3x16_bf16<false>(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), sc[i], lo, hi);
+                e4m3x16_f16(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], ref, lo, hi);
                 put(r, lo, hi);
               }
             } else {
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               for (int i = 0; i < 8; ++i) {
                 const int r = 16 * i + sub;
                 uint4 lo, hi;
-                e4m3x16_bf16<true>(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], lo, hi);
+                e4m3x16_f16(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], ref, lo, hi);
                 // what lies behind the last key must not reach the sum, whatever it is
                 if (r >= live) lo = hi = make_uint4(0, 0, 0, 0);
                 put(r, lo, hi);
@@ -343,6 +351,38 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               mbar_arrive(kv ? &v_full[s] : &k_full[s]);
               mbar_arrive(&raw_empty[kv]);
             }
+          }
+          if (key > un.key0) continue;
+          // the unit's queries, in place: |q| / 2^x < 2 for the largest of a row; rows of zeros, of f32 subnormals or
+          // with a value that is not finite as they are
+          const int rows = min(kTileRows, (p.seq_q0[un.seq + 1] - p.seq_q0[un.seq]) * p.group - un.row0);
+          for (int t = 0; t * 128 < rows; ++t) {
+            mbar_wait(&q_raw[t], n_unit[t] & 1, wg);
+            ++n_unit[t];
+            uint8_t* qt = sQ + t * T32;
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+              const int r = 16 * i + sub;
+              uint4* pa = reinterpret_cast<uint4*>(qt + tile_offset(r, e));
+              uint4* pb = reinterpret_cast<uint4*>(qt + tile_offset(r, 8 + e));
+              float a[8], b[8];
+              unpack_bf16x8(*pa, a);
+              unpack_bf16x8(*pb, b);
+              float m = fmax3_nan(amax8(a), amax8(b), 0.f);
+#pragma unroll
+              for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+              const uint32_t ex = (__float_as_uint(m) >> 23) & 255u;
+              const bool plain = ex == 0u || ex == 255u;
+              const float down = plain ? 1.f : __uint_as_float(max(1u, 254u - ex) << 23);
+              if (e == 0) q_scale[(u & 1) * 256 + t * 128 + r] = static_cast<uint8_t>(plain ? 127u : ex);
+              *pa = make_uint4(pack_half2(a[0] * down, a[1] * down), pack_half2(a[2] * down, a[3] * down),
+                               pack_half2(a[4] * down, a[5] * down), pack_half2(a[6] * down, a[7] * down));
+              *pb = make_uint4(pack_half2(b[0] * down, b[1] * down), pack_half2(b[2] * down, b[3] * down),
+                               pack_half2(b[4] * down, b[5] * down), pack_half2(b[6] * down, b[7] * down));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[t]);
           }
         }
       }
@@ -359,14 +399,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         for (int t = 0; t * 128 < rows; ++t) {
           mbar_wait(&q_empty[t], (n_unit[t] & 1) ^ 1u, wg);
           ++n_unit[t];
+          uint64_t* full = kE4m3 ? &q_raw[t] : &q_full[t];
           if (tp.q_tma) {
             // 128 / group tokens of the group's heads are the tile's rows in order; rows behind the sequence's last
             // are the next one's, or zero, and go nowhere
             if (lane == 0) {
               const int token = q0 + un.row0 / p.group + t * (128 / p.group);
-              mbar_expect_tx(&q_full[t], T32);
-              tma_load_3d(sQ + t * T32, &tp.q_map, &q_full[t], 0, un.head * p.group, token);
-              tma_load_3d(sQ + t * T32 + 16384, &tp.q_map, &q_full[t], 64, un.head * p.group, token);
+              mbar_expect_tx(full, T32);
+              tma_load_3d(sQ + t * T32, &tp.q_map, full, 0, un.head * p.group, token);
+              tma_load_3d(sQ + t * T32 + 16384, &tp.q_map, full, 64, un.head * p.group, token);
             }
           } else {
 #pragma unroll 4
@@ -379,7 +420,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[t]);
+            if (lane == 0) mbar_arrive(full);
           }
           __syncwarp();
         }
@@ -453,8 +494,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     }
     // ------------------------------------------------------------ MMA issue
     if (warp == 12) {
-      constexpr uint32_t idesc_qk = idesc_f16(128, 128, true, true, false, false);
-      constexpr uint32_t idesc_pv = idesc_f16(128, 128, true, true, false, true);
+      constexpr uint32_t idesc_qk = idesc_f16(128, 128, !kE4m3, !kE4m3, false, false);
+      constexpr uint32_t idesc_pv = idesc_f16(128, 128, !kE4m3, !kE4m3, false, true);
       const bool leader = elect_one();
       int it = 0, n_unit[2] = {0, 0}, n_p[2] = {0, 0};  // key tiles; units and key tiles per query tile
       const uint64_t q_desc = kmajor_desc(smem_u32(sQ), 0, 16384), k_desc = kmajor_desc(smem_u32(sK), 0, 16384);
@@ -530,12 +571,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + t * 128u + lane_off;
     const uint32_t tO = tmem + 256u + t * 128u + lane_off;
+    const volatile uint32_t* refs = reinterpret_cast<const volatile uint32_t*>(smem + TileSmem::kRef);
     int n_s = 0, n_unit = 0;
+    int it = 0;  // key tiles so far, over all units
     for (int u = u_begin; u < u_end; ++u) {
       const PagedUnit un = p.units[u];
       const int q0 = p.seq_q0[un.seq], q_len = p.seq_q0[un.seq + 1] - q0;
       const int unit_rows = min(kTileRows, q_len * p.group - un.row0);
-      if (t * 128 >= unit_rows) continue;
+      if (t * 128 >= unit_rows) {
+        it += (un.key1 - un.key0 + kTileKeys - 1) / kTileKeys;
+        continue;
+      }
       const int past = p.seq_kv[un.seq] - q_len, vis = p.seq_vis[un.seq];
       auto out_row_of = [&](int r) {  // row of [T, Hq] of the unit's row r
         const int rr = un.row0 + r;
@@ -545,8 +591,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       const bool live = t * 128 + row < unit_rows;
       const int limit = max(vis, past + (un.row0 + min(t * 128 + row, unit_rows - 1)) / p.group + 1);
       float m_run = -INFINITY, l_run = 0.f;
+      float q_factor = p.scale_log2;
+      int v_ref = 0;  // e4m3: largest value scale so far; O counts in units of 2^(v_ref - 127)
       bool first = true;
-      for (int key = un.key0; key < un.key1; key += kTileKeys, ++n_s) {
+      for (int key = un.key0; key < un.key1; key += kTileKeys, ++n_s, ++it) {
         mbar_wait(&s_full[t], n_s & 1, wg);
         tc_fence_after();
         const int valid = limit - key;  // keys of this tile that this row sees
@@ -560,15 +608,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           mx = full ? scores_max32<true>(s[c], mx, c * 32, valid) : scores_max32<false>(s[c], mx, c * 32, valid);
-        float m_tile = mx * p.scale_log2;
+        float scale = p.scale_log2, v_down = 0.f;
+        bool v_grow = false;
+        if constexpr (kE4m3) {
+          if (first) q_factor *= __uint_as_float(static_cast<uint32_t>((smem + TileSmem::kQScale)[(u & 1) * 256 + t * 128 + row]) << 23);
+          scale = q_factor * e8m0_value(refs[it & 3]);
+          mbar_wait(&v_full[it & 1], (it >> 1) & 1, wg);  // the values' scales; long there but for the first tile
+          const int v_tile = static_cast<int>(refs[4 + (it & 3)]);
+          if (first) v_ref = v_tile;
+          v_grow = v_tile > v_ref;
+          v_down = v_grow ? static_cast<float>(v_ref - v_tile) : 0.f;  // of what O holds
+          v_ref = max(v_ref, v_tile);
+        }
+        float m_tile = mx * scale;
         if (m_tile == INFINITY) m_tile = NAN;  // infinite scores have no softmax
         // raised by -inf -> finite, by more than 2^8, and for good by a NaN
         const bool need = !(m_tile <= m_run + kLazyRescaleLog2);
-        if (__any_sync(0xffffffffu, need)) {
+        if (__any_sync(0xffffffffu, need) || v_grow) {
           const float m_new = need ? m_tile : m_run;
           const float alpha = need ? ex2_approx(m_run - m_new) : 1.f;
           m_run = m_new;
           if (!first) {
+            const float o_down = kE4m3 ? alpha * ex2_approx(v_down) : alpha;
             // S of this tile was issued after the previous P V, which is therefore complete
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -576,35 +637,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               tmem_ld16(tO + c * 16, r);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * o_down);
               tmem_st16(tO + c * 16, r);
             }
             l_run *= alpha;
           }
         }
         first = false;
-        const float neg_m = -finite_or_zero(m_run);
+        float neg_m = -finite_or_zero(m_run), p_up = 1.f;
+        if constexpr (kE4m3) {
+          // weights relative to the largest value scale; the row sum without it
+          const float d = fmaxf(static_cast<float>(static_cast<int>(refs[4 + (it & 3)]) - v_ref), -100.f);
+          neg_m += d;
+          p_up = ex2_approx(-d);
+        }
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
           for (int c = 2 * half; c < 2 * half + 2; ++c) {
             if (full)
-              scores_exp32<true>(s[c], tS + c * 16, c * 32, valid, p.scale_log2, neg_m, sum);
+              scores_exp32<true, !kE4m3>(s[c], tS + c * 16, c * 32, valid, scale, neg_m, sum);
             else
-              scores_exp32<false>(s[c], tS + c * 16, c * 32, valid, p.scale_log2, neg_m, sum);
+              scores_exp32<false, !kE4m3>(s[c], tS + c * 16, c * 32, valid, scale, neg_m, sum);
           }
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full[2 * t + half]);
         }
-        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float tile_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l_run = kE4m3 ? fmaf(tile_sum, p_up, l_run) : l_run + tile_sum;
       }
       mbar_wait(&o_full[t], n_unit & 1, wg);
       ++n_unit;
       tc_fence_after();
       const int nsplit = un.split >> 16, split = un.split & 0xffff;
-      const float inv = nsplit == 1 ? 1.0f / l_run : 1.0f;
+      const float inv_l = nsplit == 1 ? 1.0f / l_run : 1.0f;
+      const float unit_v = kE4m3 ? e8m0_value(static_cast<uint32_t>(v_ref)) : 1.0f;
+      const float inv = inv_l * unit_v;
       const long long orow = out_row_of(min(t * 128 + row, unit_rows - 1));
       float* slot = p.part + static_cast<long long>(un.slot0 + split) * kTileSlot;
       float probe = 0.f;  // NaN if any sum is not finite
@@ -627,7 +697,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(slot + (t * 128 + row) * 128 + c * 32);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = kE4m3 ? __float_as_uint(__uint_as_float(r[4 * i + k]) * unit_v) : r[4 * i + k];
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
         __syncwarp();
       }
@@ -643,7 +718,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         const int src = __ffs(redo) - 1;
         redo &= redo - 1;
         const int lim = __shfl_sync(0xffffffffu, limit, src);
-        const float m = finite_or_zero(__shfl_sync(0xffffffffu, m_run, src)), f = __shfl_sync(0xffffffffu, inv, src);
+        const float m = finite_or_zero(__shfl_sync(0xffffffffu, m_run, src)), f = __shfl_sync(0xffffffffu, inv_l, src);
         const int r = t * 128 + (warp & 3) * 32 + src;
         const long long out_row = out_row_of(r);
         const float4 acc = row_sum_seen<kE4m3>(p, p.pages + p.seq_page0[un.seq], un.head, reinterpret_cast<const uint2*>(p.q + out_row * 16),

@@ -97,14 +97,22 @@ def write_sequences(paged, pool, table, kv_len, seed, scale=1.0):
                 getattr(pool, what + "_scale").view(torch.uint8)[ids.cuda(), :, (j % page).cuda()] = e
 
 
-def attend_tolerance(o, absv, mag):
+def attend_tolerance(o, absv, mag, small=0.0):
     """Per element. Output: half a bf16 step. Scores: f32 sums of 128 exact products, off by at most
     128 * 2^-24 of the sum of magnitudes, then scaled and shifted (3 roundings), so each weight by twice that
     relative (numerator and denominator). Weights: at most half a bf16 step each where they meet bf16
     values, their sum none. Exponential 2^-21, sums over up to 2^13 keys of f32 adds in a tree of at most 2^8
-    sequential steps: 2^-16. All times the weighted mean of |v|."""
+    sequential steps: 2^-16. All times the weighted mean of |v|. `small`: what small f16 weights add."""
     score = (128 + 3) * 2.0 ** -24 * mag
-    return HALF_BF16 * np.abs(o) + absv * (HALF_BF16 * 1.01 + 2 * score[..., None] + 2.0 ** -16) * (1 + HALF_BF16)
+    return (HALF_BF16 * np.abs(o) + absv * (HALF_BF16 * 1.01 + 2 * score[..., None] + 2.0 ** -16) + small) * (1 + HALF_BF16)
+
+
+def small_weights(kv, v):
+    """Over an 8-bit cache weights are f16 where they meet the values: those below 2^-14 are multiples of 2^-24, off by
+    at most 2^-25 (not half a step of themselves, as normal ones are). They are relative to a running max that never
+    exceeds the row's, so the row's sum that divides them is at least 1; each multiplies a value counted in units of
+    the largest scale so far, 448 of which are at most twice the largest |v|: 2^-25 * 2 max|v| a key."""
+    return v.shape[1] * 2.0 ** -24 * np.abs(v).max() if kv == "e4m3" and v.size else 0.0
 
 
 def lse_tolerance(lse, mag):
@@ -122,7 +130,7 @@ def check_attend(paged, pool, table, q, q_len, kv_len, visible, o, lse, what="",
             ref, l, absv, mag = PG.chunk_attention(as_f64(q[at + i:at + i + 1]), kk[:, :max(limit_len, visible[b])],
                                                    vv[:, :max(limit_len, visible[b])], max(limit_len, visible[b]))
             got = as_f64(o[at + i:at + i + 1])
-            tol = attend_tolerance(ref, absv, mag)
+            tol = attend_tolerance(ref, absv, mag, small_weights(pool.kv_dtype, vv))
             bad = ~(np.abs(got - ref) <= tol)
             assert not bad.any(), (what, b, i, int(bad.sum()), float(np.nanmax(np.abs(got - ref) / tol)))
             if lse is not None:
@@ -225,7 +233,8 @@ def test_attend_unseen_values_have_no_influence(cuda_ready, what, where, kv, pas
     if where:
         k, v = (sequence_rows(x, table, 0, past + where, 16) for x in pool_values(pool))
         ref, _, absv, mag = PG.chunk_attention(as_f64(q[:where]), k, v, 0)
-        assert np.all(np.abs(as_f64(o2[:where]) - ref) <= attend_tolerance(ref, absv, mag))
+        fine = np.where(np.isfinite(v), v, 0.0)
+        assert np.all(np.abs(as_f64(o2[:where]) - ref) <= attend_tolerance(ref, absv, mag, small_weights(kv, fine)))
     hit = o2[where:, 2:]
     assert not torch.isfinite(hit[..., 5]).any()
     if kv == "bf16" and what == "v":
