@@ -71,27 +71,6 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// 2^x for a pair of x <= 8 on the FMA pipe (x = j + f, as exp2_poly2) with a
-// degree-4 polynomial fitted here (relative error 2.7e-6): the row sums it
-// feeds stay good to f32.
-__device__ __forceinline__ void exp2_poly4(float& p0, float& p1, float x0, float x1) {
-  constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
-  constexpr float c0 = 9.999992614e-01f, c1 = 6.931218140e-01f, c2 = 2.402474484e-01f, c3 = 5.591786603e-02f,
-                  c4 = 9.570103830e-03f;
-  x0 = fmaxf(x0, -125.0f);
-  x1 = fmaxf(x1, -125.0f);
-  float t0, t1, j0, j1, f0, f1, q0, q1;
-  fadd2(t0, t1, x0, x1, kShift, kShift);
-  fadd2(j0, j1, t0, t1, -kShift, -kShift);
-  fadd2(f0, f1, x0, x1, -j0, -j1);
-  ffma2(q0, q1, c4, c4, f0, f1, c3, c3);
-  ffma2(q0, q1, q0, q1, f0, f1, c2, c2);
-  ffma2(q0, q1, q0, q1, f0, f1, c1, c1);
-  ffma2(q0, q1, q0, q1, f0, f1, c0, c0);
-  p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-  p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
-}
-
 // One lane of a converged warp. The MMA warp runs its loop with all lanes and
 // lets the elected one issue: under `if (lane == 0)` the compiler cannot keep
 // descriptors in uniform registers, and each tcgen05.mma then took 110 clocks to
@@ -134,41 +113,28 @@ __device__ __forceinline__ void e4m3x16_f16(const uint4& x, uint32_t b, uint32_t
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// a row's score max over 32 columns from col0; columns at or behind `valid` masked; NaN comes out as NaN
-template <bool kFull>
-__device__ __forceinline__ float scores_max32(const uint32_t (&s)[32], float m, int col0, int valid) {
+// max of 32 scores and m; NaN comes out as NaN
+__device__ __forceinline__ float scores_max32(const uint32_t (&s)[32], float m) {
   float a = m, b = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    float v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = (kFull || col0 + i + k < valid) ? __uint_as_float(s[i + k]) : -INFINITY;
-    a = fmax3_nan(a, v[0], v[1]);
-    b = fmax3_nan(b, v[2], v[3]);
+    a = fmax3_nan(a, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    b = fmax3_nan(b, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
   }
   return fmax3_nan(a, b, -INFINITY);
 }
 
 // p = 2^(s scale - m) of 32 scores as 16 pairs (bf16 or f16) at taddr; adds them to sum.
-// One pair in four takes the FMA-pipe exponential, the rest the MUFU.
-template <bool kFull, bool kBf16>
-__device__ __forceinline__ void scores_exp32(const uint32_t (&s)[32], uint32_t taddr, int col0, int valid, float scale,
-                                             float neg_m, float (&sum)[4]) {
+template <bool kBf16>
+__device__ __forceinline__ void scores_exp32(const uint32_t (&s)[32], uint32_t taddr, float scale, float neg_m,
+                                             float (&sum)[4]) {
   uint32_t pk[16];
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     float x0, x1, p0, p1;
     ffma2(x0, x1, __uint_as_float(s[i]), __uint_as_float(s[i + 1]), scale, scale, neg_m, neg_m);
-    if (((i >> 1) & 3) == 3) {
-      exp2_poly4(p0, p1, x0, x1);
-    } else {
-      p0 = ex2_approx(x0);
-      p1 = ex2_approx(x1);
-    }
-    if (!kFull) {
-      p0 = col0 + i < valid ? p0 : 0.f;
-      p1 = col0 + i + 1 < valid ? p1 : 0.f;
-    }
+    p0 = ex2_approx(x0);
+    p1 = ex2_approx(x1);
     if ((i >> 1) & 1)
       fadd2(sum[2], sum[3], sum[2], sum[3], p0, p1);
     else
@@ -326,25 +292,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 1 : 0))) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 0 : 1))) = odd ? lo : hi;
             };
-            if (live == kTileKeys) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = 16 * i + sub;
-                uint4 lo, hi;
-                e4m3x16_f16(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], ref, lo, hi);
-                put(r, lo, hi);
-              }
-            } else {
-#pragma unroll 2
-              for (int i = 0; i < 8; ++i) {
-                const int r = 16 * i + sub;
-                uint4 lo, hi;
-                e4m3x16_f16(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], ref, lo, hi);
-                // what lies behind the last key must not reach the sum, whatever it is
-                if (r >= live) lo = hi = make_uint4(0, 0, 0, 0);
-                put(r, lo, hi);
-              }
+#pragma unroll 4
+            for (int i = 0; i < 8; ++i) {
+              const int r = 16 * i + sub;
+              uint4 lo, hi;
+              e4m3x16_f16(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], ref, lo, hi);
+              put(r, lo, hi);
             }
+            // what lies behind the last key must not reach the sum, whatever it is
+            if (live < kTileKeys)
+              for (int r = sub; r < kTileKeys; r += 16)
+                if (r >= live) put(r, make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -604,10 +562,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
         tmem_ld_wait();
+        if (!full) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
+        }
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          mx = full ? scores_max32<true>(s[c], mx, c * 32, valid) : scores_max32<false>(s[c], mx, c * 32, valid);
+        for (int c = 0; c < 4; ++c) mx = scores_max32(s[c], mx);
         float scale = p.scale_log2, v_down = 0.f;
         bool v_grow = false;
         if constexpr (kE4m3) {
@@ -655,12 +619,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int c = 2 * half; c < 2 * half + 2; ++c) {
-            if (full)
-              scores_exp32<true, !kE4m3>(s[c], tS + c * 16, c * 32, valid, scale, neg_m, sum);
-            else
-              scores_exp32<false, !kE4m3>(s[c], tS + c * 16, c * 32, valid, scale, neg_m, sum);
-          }
+          for (int c = 2 * half; c < 2 * half + 2; ++c) scores_exp32<!kE4m3>(s[c], tS + c * 16, scale, neg_m, sum);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full[2 * t + half]);
