@@ -23,6 +23,8 @@ from .layer import _BF16, _F32, _dptr, _stream
 
 KV_DTYPES = {"bf16": 0, "e4m3": 1}
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 def mot_paged_create(cfg: MotPagedConfig, weights: Dict[str, torch.Tensor], stream=None) -> c_void_p:
     w = MotPagedWeights(*[_dptr(weights[n], _BF16, n) for n in ("q_norm", "k_norm")])
@@ -72,6 +74,10 @@ class MotPagedPool:
         self.kv_dtype = "e4m3" if e4m3 else "bf16"
         self.c = MotPagedPoolC(_dptr(k, kv_dtype, "k"), _dptr(v, kv_dtype, "v"), _dptr(k_scale, e8m0, "k_scale"),
                                _dptr(v_scale, e8m0, "v_scale"), k.shape[0])
+        if any(t is not None and t.device != k.device for t in (v, k_scale, v_scale)):
+            raise ValueError("a pool's tensors must be on one device")
+        self.ref = byref(self.c)
+        self.page_shape, self.device = tuple(k.shape[1:]), k.get_device()
 
 
 class MotPagedBatch:
@@ -92,6 +98,9 @@ class MotPagedBatch:
         self.batch = 0
         mot_paged_batch_set(self.handle, q_len, kv_len, table, n_pages, visible, stream)
         self.batch, self.tokens, self.kv_max = len(q_len), int(sum(q_len)), int(max(kv_len))
+        c = self.paged.cfg
+        self.q_shape = (self.tokens, c.n_q_heads, 128)
+        self.qkv_shape = (self.tokens, (c.n_q_heads + 2 * c.n_kv_heads) * 128)
 
     def workspace(self, device="cuda") -> torch.Tensor:
         if self._ws is None:
@@ -125,6 +134,11 @@ class MotPaged:
                                   float(rope_theta), max_positions, max_batch, max_tokens, max_pages)
         self.device = weights["q_norm"].device
         self.handle = mot_paged_create(self.cfg, weights, stream)
+        self._index = weights["q_norm"].get_device()
+        self._page_shape = (n_kv_heads, page_size, 128)
+        L = lib()
+        self._append, self._store, self._load, self._attend = (L.mot_paged_append, L.mot_paged_store, L.mot_paged_load,
+                                                               L.mot_paged_attend)
 
     def new_pool(self, n_pages: int) -> MotPagedPool:
         """One layer's pages, uninitialised."""
@@ -138,19 +152,31 @@ class MotPaged:
     def new_batch(self) -> MotPagedBatch:
         return MotPagedBatch(self)
 
+    # The calls below run once per layer and step, where a single token's kernel takes a few microseconds: the
+    # checks are written to cost little (plain integers for pointers, no intermediate objects).
+
     def _check(self, batch: MotPagedBatch, pool: MotPagedPool) -> None:
         if batch.paged is not self:
             raise ValueError("the batch belongs to another handle")
         if batch.batch == 0:
             raise ValueError("the batch has not been set")
-        if pool.kv_dtype != self.kv_dtype or tuple(pool.k.shape[1:]) != (self.cfg.n_kv_heads, self.cfg.page_size, 128):
-            raise ValueError(f"the pool's pages ({pool.kv_dtype}, {list(pool.k.shape[1:])}) are not this handle's")
+        if pool.kv_dtype != self.kv_dtype or pool.page_shape != self._page_shape or pool.device != self._index:
+            raise ValueError(f"the pool's pages ({pool.kv_dtype}, {list(pool.page_shape)}, device {pool.device}) are not "
+                             f"this handle's")
 
-    @staticmethod
-    def _shape(t: torch.Tensor, shape, name: str) -> torch.Tensor:
-        if tuple(t.shape) != tuple(shape):
+    def _ptr(self, t: torch.Tensor, dtype, shape, name: str) -> int:
+        """Address of a contiguous tensor of this shape and type on the handle's device."""
+        if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-        return t
+        if t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor on device {self._index} (got {t.dtype}, "
+                             f"{t.device}, strides {t.stride()})")
+        return t.data_ptr()
+
+    def _on(self, stream) -> int:
+        if stream is None:
+            return _raw_stream(self._index)
+        return _stream(stream).value or 0
 
     def append(self, batch: MotPagedBatch, qkv: torch.Tensor, pool: MotPagedPool, q: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
@@ -158,28 +184,24 @@ class MotPaged:
         keys, and writes its keys and values into the pages.
         qkv: [T, (Hq + 2 Hkv) * 128]."""
         self._check(batch, pool)
-        c = self.cfg
-        self._shape(qkv, (batch.tokens, (c.n_q_heads + 2 * c.n_kv_heads) * 128), "qkv")
         if q is None:
-            q = torch.empty(batch.tokens, c.n_q_heads, 128, dtype=_BF16, device=qkv.device)
-        self._shape(q, (batch.tokens, c.n_q_heads, 128), "q")
-        check(lib().mot_paged_append(self.handle, batch.handle, _dptr(qkv, _BF16, "qkv"), byref(pool.c),
-                                     _dptr(q, _BF16, "q"), _stream(stream)), "mot_paged_append")
+            q = torch.empty(batch.q_shape, dtype=_BF16, device=qkv.device)
+        st = self._append(self.handle, batch.handle, self._ptr(qkv, _BF16, batch.qkv_shape, "qkv"), pool.ref,
+                          self._ptr(q, _BF16, batch.q_shape, "q"), self._on(stream))
+        if st:
+            check(st, "mot_paged_append")
         return q
-
-    def _dense(self, batch, k, v):
-        rows = k.shape[2] if k.dim() == 4 else -1
-        for t, name in ((k, "k"), (v, "v")):
-            self._shape(t, (batch.batch, self.cfg.n_kv_heads, rows, 128), name)
-        return rows
 
     def store(self, batch: MotPagedBatch, k: torch.Tensor, v: torch.Tensor, pool: MotPagedPool, stream=None) -> None:
         """Dense cache k, v [batch, Hkv, rows, 128] (keys normed and rotated)
         into the pages, kv_len rows of each sequence."""
         self._check(batch, pool)
-        rows = self._dense(batch, k, v)
-        check(lib().mot_paged_store(self.handle, batch.handle, _dptr(k, _BF16, "k"), _dptr(v, _BF16, "v"), rows,
-                                    byref(pool.c), _stream(stream)), "mot_paged_store")
+        rows = k.shape[2] if k.dim() == 4 else -1
+        shape = (batch.batch, self.cfg.n_kv_heads, rows, 128)
+        st = self._store(self.handle, batch.handle, self._ptr(k, _BF16, shape, "k"), self._ptr(v, _BF16, shape, "v"),
+                         rows, pool.ref, self._on(stream))
+        if st:
+            check(st, "mot_paged_store")
 
     def load(self, batch: MotPagedBatch, pool: MotPagedPool, k: Optional[torch.Tensor] = None,
              v: Optional[torch.Tensor] = None, stream=None):
@@ -187,14 +209,17 @@ class MotPaged:
         MotAttnLayer.forward takes (rows: that of k, v when given, else the
         longest sequence's; rows behind a sequence are not written)."""
         self._check(batch, pool)
-        shape = (batch.batch, self.cfg.n_kv_heads, batch.kv_max, 128)
         if k is None:
-            k = torch.empty(shape if v is None else v.shape, dtype=_BF16, device=pool.k.device)
+            k = torch.empty((batch.batch, self.cfg.n_kv_heads, batch.kv_max, 128) if v is None else v.shape, dtype=_BF16,
+                            device=pool.k.device)
         if v is None:
             v = torch.empty_like(k)
-        rows = self._dense(batch, k, v)
-        check(lib().mot_paged_load(self.handle, batch.handle, byref(pool.c), _dptr(k, _BF16, "k"), _dptr(v, _BF16, "v"),
-                                   rows, _stream(stream)), "mot_paged_load")
+        rows = k.shape[2] if k.dim() == 4 else -1
+        shape = (batch.batch, self.cfg.n_kv_heads, rows, 128)
+        st = self._load(self.handle, batch.handle, pool.ref, self._ptr(k, _BF16, shape, "k"),
+                        self._ptr(v, _BF16, shape, "v"), rows, self._on(stream))
+        if st:
+            check(st, "mot_paged_load")
         return k, v
 
     def attend(self, batch: MotPagedBatch, q: torch.Tensor, pool: MotPagedPool, o: Optional[torch.Tensor] = None,
@@ -203,18 +228,18 @@ class MotPaged:
         """Attention of the chunk's queries [T, Hq, 128] over the pages;
         returns o [T, Hq, 128], and writes lse f32 [T, Hq] when given."""
         self._check(batch, pool)
-        shape = (batch.tokens, self.cfg.n_q_heads, 128)
-        self._shape(q, shape, "q")
+        shape = batch.q_shape
         if o is None:
             o = torch.empty_like(q)
-        self._shape(o, shape, "o")
-        if lse is not None:
-            self._shape(lse, shape[:2], "lse")
         if workspace is None:
             workspace = batch.workspace(q.device)
-        check(lib().mot_paged_attend(self.handle, batch.handle, _dptr(q, _BF16, "q"), byref(pool.c),
-                                     _dptr(o, _BF16, "o"), _dptr(lse, _F32, "lse"), _dptr(workspace, None, "workspace"),
-                                     workspace.numel(), _stream(stream)), "mot_paged_attend")
+        st = self._attend(self.handle, batch.handle, self._ptr(q, _BF16, shape, "q"), pool.ref,
+                          self._ptr(o, _BF16, shape, "o"),
+                          None if lse is None else self._ptr(lse, _F32, shape[:2], "lse"),
+                          self._ptr(workspace, workspace.dtype, workspace.shape, "workspace"),
+                          workspace.numel() * workspace.element_size(), self._on(stream))
+        if st:
+            check(st, "mot_paged_attend")
         return o
 
     def device_status(self, stream=None) -> int:
