@@ -117,8 +117,9 @@ const char* mot_dev_mlp_stage_name(int32_t id);
 /* How mot_paged_attend's work is cut over `ctas` CTAs (host-only; for tests).
  * kind 0: 8-row tiles, 1: 256-row tiles. tiles int32 [n_tiles][3]: sequence,
  * first row, keys; each stands for one tile per head. Writes units int32
- * [unit_cap][8] (sequence, head, first row, first key, end key, first partial
- * slot, number of the range | ranges << 16, counter) and cta_unit0 [ctas + 1].
+ * [unit_cap][16] (sequence, head, first row, first key, end key, first partial
+ * slot, number of the range | ranges << 16, counter, 8 more) and cta_unit0
+ * [ctas + 1].
  * MOT_ERR_UNSUPPORTED_SHAPE when unit_cap is too small. */
 mot_status mot_dev_paged_plan(int32_t kind, const int32_t* tiles, int32_t n_tiles, int32_t heads, int32_t ctas,
                               int32_t* units, int32_t unit_cap, int32_t* cta_unit0, int32_t* n_units);

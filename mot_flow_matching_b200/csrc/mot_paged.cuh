@@ -123,7 +123,7 @@ int log2_of(int v) {
 struct CutRule {
   int granule, unit_cost, min_share;
 };
-constexpr CutRule kCutRules[2] = {{kSmallWarps * kSmallGroup, 1, 3}, {kTileKeys, 2, 4}};
+constexpr CutRule kCutRules[2] = {{128, 1, 3}, {kTileKeys, 2, 4}};
 
 struct PagedTile {
   int seq, row0, keys;
@@ -152,7 +152,8 @@ bool cut_units(const std::vector<PagedTile>& tiles, int heads, int ctas, long lo
         const int take = cut ? static_cast<int>(std::min<long long>(std::max<long long>(room, 1), granules - at)) : granules;
         if (units) {
           if (n >= unit_cap) return false;
-          units[n] = PagedUnit{tl.seq, head, tl.row0, at * rule.granule, std::min(tl.keys, (at + take) * rule.granule), 0, 0, 0};
+          units[n] = PagedUnit{tl.seq, head, tl.row0, at * rule.granule, std::min(tl.keys, (at + take) * rule.granule), 0, 0, 0,
+                               0, 0, 0, 0, 0, {0, 0, 0}};
         }
         ++n;
         at += take;
@@ -226,12 +227,13 @@ PagedPool pool_view(const mot_paged_pool* p) {
                    static_cast<uint8_t*>(p->v_scale)};
 }
 
-// rows of 128 bytes, box of `box_rows` rows, as they are
-bool map_bytes(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
+// rows of 128 bytes, box of `box_rows` rows, as they are or in the 128-byte swizzle
+bool map_bytes(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows, bool swizzle) {
   const cuuint64_t dims[2] = {128, rows}, strides[1] = {128};
   const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
   return encode_ready() && g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
-                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -279,11 +281,13 @@ mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cfg->kv_dtype == MOT_PAGED_E4M3;
   set_smem_attr(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, TileSmem::bytes(e4m3));
+  const uint32_t small_smem = e4m3 ? SmallSmem<true>::kBytes : SmallSmem<false>::kBytes;
+  set_smem_attr(e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>, small_smem);
   int per_sm = 0;
   bool ok = cudaGetDevice(&h->device) == cudaSuccess &&
             cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) == cudaSuccess &&
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>,
-                                                          kSmallWarps * 32, 0) == cudaSuccess &&
+                                                          kSmallWarps * 32, small_smem) == cudaSuccess &&
             per_sm > 0 && encode_ready() && cudaMalloc(&h->gains, 256 * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&h->rope, static_cast<size_t>(cfg->max_positions) * 64 * sizeof(float2)) == cudaSuccess &&
             cudaMalloc(&h->status, sizeof(int)) == cudaSuccess;
@@ -447,6 +451,15 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
       if (!plan_units(tiles[i], c.n_kv_heads, h->ctas[i], kCutRules[i], reinterpret_cast<PagedUnit*>(w + t.units[i]),
                       t.unit_cap[i], w + t.cta_unit0[i], &n_units[i]))
         return MOT_ERR_UNSUPPORTED_SHAPE;
+      PagedUnit* units = reinterpret_cast<PagedUnit*>(w + t.units[i]);
+      for (int k = 0; k < n_units[i]; ++k) {
+        PagedUnit& un = units[k];
+        un.q0 = w[t.seq_q0 + un.seq];
+        un.rows = q_len[un.seq] * group;
+        un.past = kv_len[un.seq] - q_len[un.seq];
+        un.vis = w[t.seq_vis + un.seq];
+        un.page0 = w[t.seq_page0 + un.seq];
+      }
     }
   } catch (...) {
     return MOT_ERR_CUDA;
@@ -541,16 +554,13 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
   const mot_paged_config& c = h->cfg;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool e4m3 = c.kv_dtype == MOT_PAGED_E4M3;
+  PagedSmallParams small{};
   PagedTileParams tp{};
   PagedAttnParams& p = tp.a;
   p.q = static_cast<const uint4*>(q);
   p.o = static_cast<uint4*>(o);
   p.lse = lse;
   p.pool = pool_view(pool);
-  p.seq_q0 = bt->dev + bt->t.seq_q0;
-  p.seq_kv = bt->dev + bt->t.seq_kv;
-  p.seq_vis = bt->dev + bt->t.seq_vis;
-  p.seq_page0 = bt->dev + bt->t.seq_page0;
   p.pages = bt->dev + bt->t.pages;
   p.Hq = c.n_q_heads;
   p.Hkv = c.n_kv_heads;
@@ -565,15 +575,17 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
     p.cta_unit0 = bt->dev + bt->t.cta_unit0[i];
     p.counters = bt->dev + bt->t.counters[i];
     p.part = static_cast<float*>(workspace) + (i ? static_cast<size_t>(h->ctas[0]) * 2 * kSmallSlot : 0);
+    const uint64_t rows = static_cast<uint64_t>(pool->n_pages) * c.n_kv_heads * c.page_size;
+    CUtensorMap &km = i ? tp.k_map : small.k_map, &vm = i ? tp.v_map : small.v_map;
+    const uint32_t box = i ? c.page_size : 16;
+    if (e4m3 ? !map_bytes(&km, pool->k, rows, box, i == 0) || !map_bytes(&vm, pool->v, rows, box, i == 0)
+             : !map2d(&km, pool->k, true, 128, rows, 128, box) || !map2d(&vm, pool->v, true, 128, rows, 128, box))
+      return MOT_ERR_CUDA;
     if (i == 0) {
-      e = launch_pdl(e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>, dim3(h->ctas[0]),
-                     dim3(kSmallWarps * 32), 0, st, p);
+      small.a = p;
+      e = e4m3 ? launch_pdl(paged_attn_small_kernel<true>, dim3(h->ctas[0]), dim3(kSmallWarps * 32), SmallSmem<true>::kBytes, st, small)
+               : launch_pdl(paged_attn_small_kernel<false>, dim3(h->ctas[0]), dim3(kSmallWarps * 32), SmallSmem<false>::kBytes, st, small);
     } else {
-      const uint64_t rows = static_cast<uint64_t>(pool->n_pages) * c.n_kv_heads * c.page_size;
-      if (e4m3 ? !map_bytes(&tp.k_map, pool->k, rows, c.page_size) || !map_bytes(&tp.v_map, pool->v, rows, c.page_size)
-               : !map2d(&tp.k_map, pool->k, true, 128, rows, 128, c.page_size) ||
-                     !map2d(&tp.v_map, pool->v, true, 128, rows, 128, c.page_size))
-        return MOT_ERR_CUDA;
       // a tile's 128 rows are whole tokens where the group divides 128: one box
       tp.q_tma = 128 % p.group == 0;
       const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(c.n_q_heads), static_cast<cuuint64_t>(bt->tokens)};

@@ -301,20 +301,37 @@ __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__
 // ---------------------------------------------------------------- attention, few rows
 // A unit is a tile of query rows of one (sequence, KV head) and a range of its
 // keys. Query rows are (token, head of the group) pairs, head fastest, so the
-// tile reads the KV head's keys once for the whole group.
-struct PagedUnit {
+// tile reads the KV head's keys once for the whole group. The record holds all
+// that a CTA has to know of the sequence, so that it is one load away.
+struct __align__(16) PagedUnit {
   int seq, head, row0, key0, key1;
-  int slot0;   // first partial slot of the tile (nsplit > 1)
-  int split;   // this range's number | nsplit << 16
-  int counter; // arrival counter of the tile
+  int slot0;    // first partial slot of the tile (nsplit > 1)
+  int split;    // this range's number | nsplit << 16
+  int counter;  // arrival counter of the tile
+  int q0;       // first token of the chunk in the packed tensors
+  int rows;     // query rows of the chunk
+  int past;     // position of its first token
+  int vis;      // keys that all its queries see
+  int page0;    // first entry of the sequence in the page list
+  int pad[3];
 };
+
+// a record, read anew (not kept in registers from an earlier read)
+__device__ __forceinline__ PagedUnit read_unit(const PagedUnit* u) {
+  PagedUnit r;
+  int* w = reinterpret_cast<int*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3]) : "l"(reinterpret_cast<const int4*>(u) + i));
+  return r;
+}
 
 struct PagedAttnParams {
   const uint4* q;  // bf16 [T, Hq, 128]
   uint4* o;        // bf16 [T, Hq, 128]
   float* lse;      // [T, Hq] or null
   PagedPool pool;
-  const int *seq_q0, *seq_kv, *seq_vis, *seq_page0, *pages;
+  const int* pages;
   const PagedUnit* units;
   const int* cta_unit0;  // units of CTA i: [cta_unit0[i], cta_unit0[i + 1])
   int* counters;
@@ -350,35 +367,53 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 
 constexpr int kSmallRows = 8;     // query rows of a unit
 constexpr int kSmallWarps = 8;
-constexpr int kSmallGroup = 16;   // keys a warp takes at a time
 constexpr int kSmallSlot = kSmallRows * 128 + kSmallRows * 2;  // floats of a partial
 
-// One 16-key group's registers: keys as the A operand of S^T = K Q^T (lane
-// (g, c) = (lane / 4, lane % 4) holds keys g and g + 8), values as the A operand
-// of O^T += V^T P^T (keys 2c, 2c+1, 2c+8, 2c+9). The dims each register pair
-// stands for are permuted so that every lane loads whole 16-byte pieces and a
-// warp's load covers whole sectors; the same permutation is applied to Q, and the
+struct PagedSmallParams {
+  CUtensorMap k_map, v_map;  // 2D rows of the pool, box of 16 rows x 128 bytes, 128-byte swizzle
+  PagedAttnParams a;
+};
+
+// Per warp a ring of pieces, each the keys or the values of 16 tokens: 12 KB in
+// flight a warp, 192 KB an SM, whatever the type.
+template <bool kE4m3>
+struct SmallSmem {
+  static constexpr int kPieceBytes = kE4m3 ? 2048 : 4096;
+  static constexpr int kPieces = kE4m3 ? 6 : 3;
+  static constexpr uint32_t kRing = kSmallWarps * kPieces * kPieceBytes;
+  static constexpr uint32_t kBytes = kRing + 1024;
+};
+
+// 16 keys' registers: keys as the A operand of S^T = K Q^T (lane (g, c) =
+// (lane / 4, lane % 4) holds keys g and g + 8), values as the A operand of
+// O^T += V^T P^T (keys 2c, 2c+1, 2c+8, 2c+9). The rows lie in shared memory in
+// 128-byte lines whose 16-byte pieces are permuted by row & 7. The dims each
+// register pair stands for are permuted so that every lane reads whole pieces
+// and eight lanes hit all banks once: keys, pieces 2c, 2c+1 (and those of the
+// second line); values, piece g. The same permutation is applied to Q, and the
 // permuted rows of O^T are consecutive dims of a lane.
 template <bool kE4m3>
 struct KvGroup;
 
 template <>
-struct KvGroup<false> {
+struct KvGroup<false> {  // two lines a row: dims 0-63 of the 16 rows, then dims 64-127
   uint4 k[2][4];
   uint4 v[4][2];
-  __device__ __forceinline__ void load_k(const PagedPool& p, long long row, int g, int c) {
+  __device__ __forceinline__ void read_k(const uint8_t* s, int g, int c) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        k[r][i] = __ldg(reinterpret_cast<const uint4*>(p.k) + (row + g + 8 * r) * 16 + 4 * i + c);
+        k[r][i] = *reinterpret_cast<const uint4*>(s + (i >> 1) * 2048 + (g + 8 * r) * 128 + (((2 * c + (i & 1)) ^ g) << 4));
   }
-  __device__ __forceinline__ void load_v(const PagedPool& p, long long row, int g, int c) {
+  __device__ __forceinline__ void read_v(const uint8_t* s, int g, int c) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int i = 0; i < 4; ++i) {
+      const int row = 2 * c + (i & 1) + 8 * (i >> 1);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        v[s][j] = __ldg(reinterpret_cast<const uint4*>(p.v) + (row + 2 * c + (s & 1) + 8 * (s >> 1)) * 16 + 8 * j + g);
+        v[i][j] = *reinterpret_cast<const uint4*>(s + j * 2048 + row * 128 + ((g ^ (row & 7)) << 4));
+    }
   }
 };
 
@@ -387,21 +422,19 @@ struct KvGroup<true> {
   uint4 k[2][2];
   uint4 v[4];
   uint32_t ks[2], vs[2];  // scale bytes of keys g, g + 8
-  __device__ __forceinline__ void load_k(const PagedPool& p, long long row, int g, int c) {
+  __device__ __forceinline__ void read_k(const uint8_t* s, int g, int c) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        k[r][i] = __ldg(reinterpret_cast<const uint4*>(p.k) + (row + g + 8 * r) * 8 + 4 * i + c);
-      ks[r] = __ldg(p.ks + row + g + 8 * r);
-    }
+        k[r][i] = *reinterpret_cast<const uint4*>(s + (g + 8 * r) * 128 + (((2 * c + i) ^ g) << 4));
   }
-  __device__ __forceinline__ void load_v(const PagedPool& p, long long row, int g, int c) {
+  __device__ __forceinline__ void read_v(const uint8_t* s, int g, int c) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      v[s] = __ldg(reinterpret_cast<const uint4*>(p.v) + (row + 2 * c + (s & 1) + 8 * (s >> 1)) * 8 + g);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) vs[r] = __ldg(p.vs + row + g + 8 * r);
+    for (int i = 0; i < 4; ++i) {
+      const int row = 2 * c + (i & 1) + 8 * (i >> 1);
+      v[i] = *reinterpret_cast<const uint4*>(s + row * 128 + ((g ^ (row & 7)) << 4));
+    }
   }
 };
 
@@ -416,9 +449,7 @@ __device__ __forceinline__ void set_word(uint4& v, int i, uint32_t w) {
 // Values of a group that only some of the tile's rows see: an infinity or NaN
 // times a zero weight would reach the rows that do not see it, so it is taken
 // out (set to zero) and its key remembered per dim; rows whose limit is past
-// that key get NaN at the end. Rare: any non-finite value at all ends in NaNs.
-__device__ __noinline__ void note_poison(int* poison, int dim, int key) { atomicMin(poison + dim, key); }
-
+// that key get NaN at the end.
 template <bool kE4m3>
 __device__ __forceinline__ void take_out_poison(KvGroup<kE4m3>& kv, int* poison, int key0, int g, int c) {
   if constexpr (!kE4m3) {
@@ -432,11 +463,11 @@ __device__ __forceinline__ void take_out_poison(KvGroup<kE4m3>& kv, int* poison,
           const int key = key0 + 2 * c + (s & 1) + 8 * (s >> 1);
           const int dim = 64 * j + 8 * g + 2 * i;
           if ((w & 0x7f80u) == 0x7f80u) {
-            note_poison(poison, dim, key);
+            atomicMin(poison + dim, key);
             w &= 0xffff0000u;
           }
           if ((w & 0x7f800000u) == 0x7f800000u) {
-            note_poison(poison, dim + 1, key);
+            atomicMin(poison + dim + 1, key);
             w &= 0xffffu;
           }
           set_word(kv.v[s][j], i, w);
@@ -445,7 +476,8 @@ __device__ __forceinline__ void take_out_poison(KvGroup<kE4m3>& kv, int* poison,
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       if (kv.vs[r] == 255u) {
-        for (int d = 0; d < 32; ++d) note_poison(poison, 32 * c + d, key0 + g + 8 * r);
+#pragma unroll 1
+        for (int d = 0; d < 32; ++d) atomicMin(poison + 32 * c + d, key0 + g + 8 * r);
         kv.vs[r] = 0u;
       }
 #pragma unroll
@@ -456,7 +488,7 @@ __device__ __forceinline__ void take_out_poison(KvGroup<kE4m3>& kv, int* poison,
 #pragma unroll
         for (int b = 0; b < 4; ++b)
           if (((w >> (8 * b)) & 0x7fu) == 0x7fu) {
-            note_poison(poison, 16 * g + 4 * i + b, key0 + 2 * c + (s & 1) + 8 * (s >> 1));
+            atomicMin(poison + 16 * g + 4 * i + b, key0 + 2 * c + (s & 1) + 8 * (s >> 1));
             w &= ~(0xffu << (8 * b));
           }
         set_word(kv.v[s], i, w);
@@ -483,41 +515,81 @@ __device__ __forceinline__ void clear_tail(KvGroup<kE4m3>& kv, int live, int g, 
 }
 
 // Attention of up to 8 query rows per unit over a range of keys; bound by the
-// bytes of the pages. Each warp takes 16 keys at a time straight into
-// registers (no shared memory, no barrier in the loop) and keeps its own running
-// max, sum and O^T; the warps' results are merged through shared memory, the
-// ranges' results by whichever CTA arrives last, in the order of the ranges.
+// bytes of the pages. Each warp streams its own keys, 16 at a time, through its
+// own ring in shared memory (TMA, one barrier a piece, nothing shared between
+// the warps in the loop) and keeps its own running max, sum and O^T; the warps'
+// results are merged through shared memory, the ranges' results by whichever CTA
+// arrives last, in the order of the ranges.
 // Tensor-core shapes: S^T (16 keys x 8 rows) = K Q^T and O^T (128 dims x 8
 // rows) += V^T P^T, so the keys and values are the 16-row operand and no row is
 // wasted on padding to 16 query rows; P^T gets into operand layout by
 // movmatrix. bf16 pages: P is split into two bf16 (hi + lo), whose products sum
-// in f32, so that the weights are not rounded to 8 bits. e4m3 pages: keys and values become f16 exactly, the
-// scales are applied in f32 to the scores and to the weights (relative to the
-// largest value scale so far, so that a weight in f16 neither overflows nor
-// loses the keys that count); queries are scaled by a power of two into f16.
+// in f32, so that the weights are not rounded to 8 bits. e4m3 pages: keys and
+// values become f16 exactly, the scales are applied in f32 to the scores and to
+// the weights (relative to the largest value scale so far, so that a weight in
+// f16 neither overflows nor loses the keys that count); queries are scaled by a
+// power of two into f16.
+// The batch's tables are written by copies, never by a kernel, so they are read
+// before the grid this one depends on has completed.
 template <bool kE4m3>
-__global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(const __grid_constant__ PagedAttnParams p) {
-  __shared__ float s_o[kSmallWarps][kSmallRows][132];
+__global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
+  using SM = SmallSmem<kE4m3>;
+  const PagedAttnParams& p = sp.a;
+  extern __shared__ uint8_t smem_raw[];
   __shared__ float2 s_ml[kSmallWarps][kSmallRows];
   __shared__ int s_poison[128];
   __shared__ int s_last;
+  __shared__ uint32_t s_abort;
+  __shared__ uint64_t s_bar[kSmallWarps][SM::kPieces];
   grid_dep_launch();
-  grid_dep_wait();
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, c = lane & 3;
-  const int page_mask = (1 << p.page_shift) - 1;
-  const int u_end = p.cta_unit0[blockIdx.x + 1];
-  for (int u = p.cta_unit0[blockIdx.x]; u < u_end; ++u) {
+  uint8_t* rings = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = rings + warp * (SM::kPieces * SM::kPieceBytes);
+  // a warp's sums for the merge lie in its ring, which is idle by then: [8 rows][132]
+  auto sums = [&](int w, int r) { return reinterpret_cast<float*>(rings + w * (SM::kPieces * SM::kPieceBytes)) + r * 132; };
+  uint64_t* bars = s_bar[warp];
+  const int u_begin = p.cta_unit0[blockIdx.x], u_end = p.cta_unit0[blockIdx.x + 1];
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < SM::kPieces; ++i) mbar_init(&bars[i], 1);
+    if (warp == 0) s_abort = 0u;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const WaitGuard wg{&s_abort, p.status};
+  int slot = 0;        // ring position of the next piece to be read
+  uint32_t phase = 0;  // and its phase
+  for (int u = u_begin; u < u_end; ++u) {
     const PagedUnit un = p.units[u];
-    const int q0 = p.seq_q0[un.seq], q_len = p.seq_q0[un.seq + 1] - q0, kv_len = p.seq_kv[un.seq];
-    const int vis = p.seq_vis[un.seq];
-    const int* pages = p.pages + p.seq_page0[un.seq];
-    const int rows = min(kSmallRows, q_len * p.group - un.row0);
-    const int past = kv_len - q_len;
-    auto limit_of = [&](int r) { return max(vis, past + (un.row0 + min(r, rows - 1)) / p.group + 1); };
+    const int rows = min(kSmallRows, un.rows - un.row0);
+    auto limit_of = [&](int r) { return max(un.vis, un.past + (un.row0 + min(r, rows - 1)) / p.group + 1); };
     const int lim_min = limit_of(0), lim_max = limit_of(rows - 1);
-    const int lim[2] = {limit_of(2 * c), limit_of(2 * c + 1)};
-    for (int i = threadIdx.x; i < 128; i += kSmallWarps * 32) s_poison[i] = INT_MAX;
-    __syncthreads();
+    // this warp's groups of 16 keys: un.key0 + 16 warp + 128 n; lane i looks up the pool row of group n0 + i
+    const int key0 = un.key0 + 16 * warp;
+    const int groups = max(0, (un.key1 - key0 + 16 * kSmallWarps - 1) / (16 * kSmallWarps));
+    auto row_at = [&](int n) {
+      const int key = key0 + min(n, groups - 1) * (16 * kSmallWarps);
+      return ((p.pages[un.page0 + (key >> p.page_shift)] * p.Hkv + un.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+    };
+    int rows_now = groups > 0 ? row_at(lane) : 0, rows_next = groups > 32 ? row_at(32 + lane) : 0;
+    if (lim_max != lim_min)
+      for (int i = threadIdx.x; i < 128; i += kSmallWarps * 32) s_poison[i] = INT_MAX;
+    if (u == u_begin) grid_dep_wait();
+    // pieces are numbered keys 0, values 0, keys 1, ...; piece i goes to ring position (slot now + i) % kPieces
+    auto load_piece = [&](int i, int n_base, int at) {
+      const int n = (i >> 1) - n_base;
+      const int row = __shfl_sync(0xffffffffu, n < 32 ? rows_now : rows_next, n & 31);
+      if (lane == 0) {
+        uint8_t* dst = ring + at * SM::kPieceBytes;
+        const CUtensorMap* map = (i & 1) ? &sp.v_map : &sp.k_map;
+        mbar_expect_tx(&bars[at], SM::kPieceBytes);
+        tma_load_2d(dst, map, &bars[at], 0, row);
+        if (!kE4m3) tma_load_2d(dst + 2048, map, &bars[at], 64, row);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < SM::kPieces; ++i)
+      if (i < 2 * groups) load_piece(i, 0, slot + i < SM::kPieces ? slot + i : slot + i - SM::kPieces);
 
     // this lane's piece of query row g, in the dims order of the key registers
     uint32_t q[16];
@@ -525,11 +597,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
     {
       const int rr = un.row0 + g;
       const bool live = g < rows;
-      const uint4* src = p.q + (static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group) * 16;
+      const uint4* src = p.q + (static_cast<long long>(un.q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group) * 16;
       uint4 w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int piece = kE4m3 ? 8 * (i >> 1) + 2 * c + (i & 1) : 4 * i + c;
+        const int piece = kE4m3 ? 4 * c + i : 8 * (i >> 1) + 2 * c + (i & 1);
         w[i] = live ? __ldg(src + piece) : make_uint4(0, 0, 0, 0);
       }
       if (!kE4m3) {
@@ -564,31 +636,39 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
       for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     int v_ref = 0;  // largest value scale byte so far (e4m3)
-
-    KvGroup<kE4m3> kv;
-    const int key_last = un.key1;
-    int key = un.key0 + warp * kSmallGroup;
-    auto row_of = [&](int k) {
-      return ((static_cast<long long>(pages[k >> p.page_shift]) * p.Hkv + un.head) << p.page_shift) + (k & page_mask);
+    uint32_t scales = 0;  // bytes: key scales of keys g, g + 8, value scales of the same (e4m3)
+    auto scales_of = [&](int n, int n_base) {
+      const int row = __shfl_sync(0xffffffffu, n - n_base < 32 ? rows_now : rows_next, (n - n_base) & 31) + g;
+      return static_cast<uint32_t>(__ldg(p.pool.ks + row)) | static_cast<uint32_t>(__ldg(p.pool.ks + row + 8)) << 8 |
+             static_cast<uint32_t>(__ldg(p.pool.vs + row)) << 16 | static_cast<uint32_t>(__ldg(p.pool.vs + row + 8)) << 24;
     };
-    long long row = 0;
-    if (key < key_last) {
-      row = row_of(key);
-      kv.load_k(p.pool, row, g, c);
-      kv.load_v(p.pool, row, g, c);
-    }
-    while (key < key_last) {
-      const int next = key + kSmallWarps * kSmallGroup;
-      const long long row_next = next < key_last ? row_of(next) : 0;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      float kf[2] = {1.f, 1.f};
+    if (kE4m3 && groups > 0) scales = scales_of(0, 0);
+
+    if (lim_max != lim_min) __syncthreads();  // s_poison
+    int n_base = 0;  // rows_now holds groups n_base.., rows_next those 32 behind
+    for (int n = 0; n < groups; ++n) {
+      const int key = key0 + n * (16 * kSmallWarps);
+      if (n - n_base == 32) {
+        n_base = n;
+        rows_now = rows_next;
+        rows_next = groups - n > 32 ? row_at(n + 32 + lane) : 0;
+      }
+      KvGroup<kE4m3> kv;
+      const uint32_t sc = scales;
+      mbar_wait(&bars[slot], phase, wg);
+      kv.read_k(ring + slot * SM::kPieceBytes, g, c);
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, x[4];
+      // base-2 scores; x[0], x[1]: key g, rows 2c, 2c + 1; x[2], x[3]: key g + 8
       if constexpr (!kE4m3) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           mma_16816<true>(s, kv.k[0][i].x, kv.k[1][i].x, kv.k[0][i].y, kv.k[1][i].y, q[4 * i], q[4 * i + 1]);
           mma_16816<true>(s, kv.k[0][i].z, kv.k[1][i].z, kv.k[0][i].w, kv.k[1][i].w, q[4 * i + 2], q[4 * i + 3]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = s[i] * qf[i & 1];
       } else {
+        if (n + 1 < groups) scales = scales_of(n + 1, n_base);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -597,19 +677,25 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
             mma_16816<false>(s, e4m3x2_f16x2(a), e4m3x2_f16x2(b), e4m3x2_f16x2(a >> 16), e4m3x2_f16x2(b >> 16),
                              q[8 * i + 2 * h], q[8 * i + 2 * h + 1]);
           }
-        kf[0] = e8m0_value(kv.ks[0]);
-        kf[1] = e8m0_value(kv.ks[1]);
-      }
-      if (next < key_last) kv.load_k(p.pool, row_next, g, c);
-      // base-2 scores; s[0], s[1]: key g, rows 2c, 2c + 1; s[2], s[3]: key g + 8
-      float x[4];
+        const float kf[2] = {e8m0_value(sc & 255u), e8m0_value((sc >> 8) & 255u)};
+        kv.vs[0] = (sc >> 16) & 255u;
+        kv.vs[1] = sc >> 24;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = s[i] * (kE4m3 ? qf[i & 1] * kf[i >> 1] : qf[i & 1]);
-      const bool whole = key + kSmallGroup <= lim_min;
-      if (!whole) {
+        for (int i = 0; i < 4; ++i) x[i] = s[i] * (qf[i & 1] * kf[i >> 1]);
+      }
+      __syncwarp();
+      if (2 * n + SM::kPieces < 2 * groups) load_piece(2 * n + SM::kPieces, n_base, slot);
+      if (++slot == SM::kPieces) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      mbar_wait(&bars[slot], phase, wg);
+      kv.read_v(ring + slot * SM::kPieceBytes, g, c);
+      if (key + 16 > lim_min) {
+        const int lim0 = limit_of(2 * c), lim1 = limit_of(2 * c + 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (key + g + 8 * (i >> 1) >= lim[i & 1]) x[i] = -INFINITY;
+          if (key + g + 8 * (i >> 1) >= ((i & 1) ? lim1 : lim0)) x[i] = -INFINITY;
         clear_tail<kE4m3>(kv, lim_max - key, g, c);
         if (lim_max != lim_min) take_out_poison<kE4m3>(kv, s_poison, key, g, c);
       }
@@ -661,9 +747,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
           const uint32_t sel = (t & 1) ? 0x7632u : 0x5410u;
           uint32_t a[4];  // dims 8g + t and 64 + 8g + t; keys 2c, 2c+1 and 2c+8, 2c+9
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            a[j] = __byte_perm(word(kv.v[0][j], t >> 1), word(kv.v[1][j], t >> 1), sel);
-            a[2 + j] = __byte_perm(word(kv.v[2][j], t >> 1), word(kv.v[3][j], t >> 1), sel);
+          for (int h = 0; h < 2; ++h) {
+            a[h] = __byte_perm(word(kv.v[0][h], t >> 1), word(kv.v[1][h], t >> 1), sel);
+            a[2 + h] = __byte_perm(word(kv.v[2][h], t >> 1), word(kv.v[3][h], t >> 1), sel);
           }
           mma_16816<true>(o[t], a[0], a[1], a[2], a[3], b0, b1);
           mma_16816<true>(o[t], a[0], a[1], a[2], a[3], d0, d1);
@@ -682,12 +768,12 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
           // word i of the low and of the high half: dims 16g + 4i.. and 16g + 8 + 4i..
           uint32_t e[2][2][2];  // [dim half][key pair][dims 0,1 | 2,3]: bytes (key a, key b) per dim
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int kp = 0; kp < 2; ++kp) {
-              const uint32_t a = word(kv.v[2 * kp], 2 * j + i), b = word(kv.v[2 * kp + 1], 2 * j + i);
-              e[j][kp][0] = __byte_perm(a, b, 0x5140);
-              e[j][kp][1] = __byte_perm(a, b, 0x7362);
+              const uint32_t a = word(kv.v[2 * kp], 2 * h + i), b = word(kv.v[2 * kp + 1], 2 * h + i);
+              e[h][kp][0] = __byte_perm(a, b, 0x5140);
+              e[h][kp][1] = __byte_perm(a, b, 0x7362);
             }
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
@@ -697,11 +783,16 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
           }
         }
       }
-      if (next < key_last) kv.load_v(p.pool, row_next, g, c);
-      key = next;
+      __syncwarp();
+      if (2 * n + 1 + SM::kPieces < 2 * groups) load_piece(2 * n + 1 + SM::kPieces, n_base, slot);
+      if (++slot == SM::kPieces) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
 
     // merge of the warps
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -714,7 +805,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
       if (g == 0) s_ml[warp][r] = make_float2(m_run[i], l_run[i]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float* dst = &s_o[warp][r][kE4m3 ? 16 * g + 8 * j : 64 * j + 8 * g];
+        float* dst = sums(warp, r) + (kE4m3 ? 16 * g + 8 * j : 64 * j + 8 * g);
 #pragma unroll
         for (int t = 0; t < 8; t += 4)
           *reinterpret_cast<float4*>(dst + t) = make_float4(o[t][2 * j + i] * unscale, o[t + 1][2 * j + i] * unscale,
@@ -726,9 +817,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
     const int r = warp;  // one warp per row
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float2 ml, const float4 v) {
-      const float w = ex2_approx(ml.x - finite_or_zero(m));
-      l = fmaf(ml.y, w, l);
+    auto add = [&](float w, const float4 v) {
       acc.x = fmaf(v.x, w, acc.x);
       acc.y = fmaf(v.y, w, acc.y);
       acc.z = fmaf(v.z, w, acc.z);
@@ -737,8 +826,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
     if (r < rows) {
 #pragma unroll
       for (int i = 0; i < kSmallWarps; ++i) m = fmaxf(m, s_ml[i][r].x);
+      const float m0 = finite_or_zero(m);
 #pragma unroll
-      for (int i = 0; i < kSmallWarps; ++i) add(s_ml[i][r], *reinterpret_cast<const float4*>(&s_o[i][r][4 * lane]));
+      for (int i = 0; i < kSmallWarps; ++i) {
+        const float2 ml = s_ml[i][r];
+        const float w = ex2_approx(ml.x - m0);
+        l = fmaf(ml.y, w, l);
+        add(w, *reinterpret_cast<const float4*>(sums(i, r) + 4 * lane));
+      }
       if (lim_max != lim_min) {
         const int lr = limit_of(r);
         if (s_poison[4 * lane] < lr) acc.x = NAN;
@@ -754,41 +849,64 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
         reinterpret_cast<float4*>(slot + r * 128)[lane] = acc;
         if (lane == 0) reinterpret_cast<float2*>(slot + kSmallRows * 128)[r] = make_float2(m, l);
       }
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        // wraps to 0 with the last arrival: ready for the next call
+        // one fence for the CTA's writes, which the barrier put before it; the counter wraps to 0 with the last
+        // arrival: ready for the next call
+        __threadfence();
         s_last = atomicInc(reinterpret_cast<unsigned*>(p.counters) + un.counter, nsplit - 1) == nsplit - 1;
         __threadfence();
       }
       __syncthreads();
       write = write && s_last;
       if (write) {
+        // lane i holds the max and sum of range 32 b + i; the sums of eight ranges are in flight at a time
         const float* slot = p.part + static_cast<long long>(un.slot0) * kSmallSlot;
-        float mm = -INFINITY;
-        for (int i = lane; i < nsplit; i += 32)
-          mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(slot + static_cast<long long>(i) * kSmallSlot + kSmallRows * 128) + r).x);
+        auto ml_of = [&](int i) {
+          return i < nsplit ? __ldcg(reinterpret_cast<const float2*>(slot + static_cast<long long>(i) * kSmallSlot + kSmallRows * 128) + r)
+                            : make_float2(-INFINITY, 0.f);
+        };
+        const float2 first = ml_of(lane);
+        m = first.x;
+        for (int b = 32; b < nsplit; b += 32) m = fmaxf(m, ml_of(b + lane).x);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-        m = mm;
+        for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float m0 = finite_or_zero(m);
         l = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < nsplit; ++i) {
-          const float* sl = slot + static_cast<long long>(i) * kSmallSlot;
-          add(__ldcg(reinterpret_cast<const float2*>(sl + kSmallRows * 128) + r), __ldcg(reinterpret_cast<const float4*>(sl + r * 128) + lane));
+        for (int b = 0; b < nsplit; b += 32) {
+          const float2 ml = b == 0 ? first : ml_of(b + lane);
+          const float wl = ex2_approx(ml.x - m0);
+          float part_l = b + lane < nsplit ? ml.y * wl : 0.f;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, d);
+          l += part_l;
+          const int n = min(32, nsplit - b);
+          for (int i = 0; i < n; i += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              v[k] = __ldcg(reinterpret_cast<const float4*>(slot + static_cast<long long>(b + min(i + k, n - 1)) * kSmallSlot + r * 128) + lane);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float w = __shfl_sync(0xffffffffu, wl, i + k);
+              if (i + k < n) add(w, v[k]);
+            }
+          }
         }
       }
     }
     if (write) {
       const int rr = un.row0 + r;
-      const long long out_row = static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
+      const long long out_row = static_cast<long long>(un.q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
       const float inv = 1.0f / l;
       reinterpret_cast<uint2*>(p.o + out_row * 16)[lane] = make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
       if (p.lse && lane == 0) p.lse[out_row] = lse_of(m, l);
     }
+    fence_proxy_async_smem();  // the rings go back to the TMA
     __syncthreads();
   }
+  if (u_begin == u_end) grid_dep_wait();
 }
 
 }  // namespace mot

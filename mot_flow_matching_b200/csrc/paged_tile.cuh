@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           if (key > un.key0) continue;
           // the unit's queries, in place: |q| / 2^x < 2 for the largest of a row; rows of zeros, of f32 subnormals or
           // with a value that is not finite as they are
-          const int rows = min(kTileRows, (p.seq_q0[un.seq + 1] - p.seq_q0[un.seq]) * p.group - un.row0);
+          const int rows = min(kTileRows, un.rows - un.row0);
           for (int t = 0; t * 128 < rows; ++t) {
             mbar_wait(&q_raw[t], n_unit[t] & 1, wg);
             ++n_unit[t];
@@ -352,8 +352,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       int n_unit[2] = {0, 0};
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
-        const int q0 = p.seq_q0[un.seq];
-        const int rows = min(kTileRows, (p.seq_q0[un.seq + 1] - q0) * p.group - un.row0);
+        const int q0 = un.q0;
+        const int rows = min(kTileRows, un.rows - un.row0);
         for (int t = 0; t * 128 < rows; ++t) {
           mbar_wait(&q_empty[t], (n_unit[t] & 1) ^ 1u, wg);
           ++n_unit[t];
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       int it = 0, tails = 0;  // key tiles so far, over all units
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
-        const int* pages = p.pages + p.seq_page0[un.seq];
+        const int* pages = p.pages + un.page0;
         for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
           const int s = it & 1;
           const uint32_t ph = (it >> 1) & 1;
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       };
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
-        const int rows = (p.seq_q0[un.seq + 1] - p.seq_q0[un.seq]) * p.group - un.row0;
+        const int rows = un.rows - un.row0;
         const int nt = rows > 128 ? 2 : 1;
         const int tiles = (un.key1 - un.key0 + kTileKeys - 1) / kTileKeys;
         for (int j = 0; j < tiles; ++j, ++it) {
@@ -533,26 +533,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     int n_s = 0, n_unit = 0;
     int it = 0;  // key tiles so far, over all units
     for (int u = u_begin; u < u_end; ++u) {
-      const PagedUnit un = p.units[u];
-      const int q0 = p.seq_q0[un.seq], q_len = p.seq_q0[un.seq + 1] - q0;
-      const int unit_rows = min(kTileRows, q_len * p.group - un.row0);
-      if (t * 128 >= unit_rows) {
-        it += (un.key1 - un.key0 + kTileKeys - 1) / kTileKeys;
+      int key0, key1, limit;
+      bool active;
+      {
+        const PagedUnit un = read_unit(p.units + u);
+        key0 = un.key0;
+        key1 = un.key1;
+        const int unit_rows = min(kTileRows, un.rows - un.row0);
+        active = t * 128 < unit_rows;
+        limit = max(un.vis, un.past + (un.row0 + min(t * 128 + row, unit_rows - 1)) / p.group + 1);
+      }
+      if (!active) {
+        it += (key1 - key0 + kTileKeys - 1) / kTileKeys;
         continue;
       }
-      const int past = p.seq_kv[un.seq] - q_len, vis = p.seq_vis[un.seq];
-      auto out_row_of = [&](int r) {  // row of [T, Hq] of the unit's row r
-        const int rr = un.row0 + r;
-        return static_cast<long long>(q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
-      };
-      // 16 lanes a row, two rows at a time
-      const bool live = t * 128 + row < unit_rows;
-      const int limit = max(vis, past + (un.row0 + min(t * 128 + row, unit_rows - 1)) / p.group + 1);
       float m_run = -INFINITY, l_run = 0.f;
       float q_factor = p.scale_log2;
       int v_ref = 0;  // e4m3: largest value scale so far; O counts in units of 2^(v_ref - 127)
       bool first = true;
-      for (int key = un.key0; key < un.key1; key += kTileKeys, ++n_s, ++it) {
+      for (int key = key0; key < key1; key += kTileKeys, ++n_s, ++it) {
         mbar_wait(&s_full[t], n_s & 1, wg);
         tc_fence_after();
         const int valid = limit - key;  // keys of this tile that this row sees
@@ -630,6 +629,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       mbar_wait(&o_full[t], n_unit & 1, wg);
       ++n_unit;
       tc_fence_after();
+      const PagedUnit un = read_unit(p.units + u);
+      const int unit_rows = min(kTileRows, un.rows - un.row0);
+      const bool live = t * 128 + row < unit_rows;
+      auto out_row_of = [&](int r) {  // row of [T, Hq] of the unit's row r
+        const int rr = un.row0 + r;
+        return static_cast<long long>(un.q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
+      };
       const int nsplit = un.split >> 16, split = un.split & 0xffff;
       const float inv_l = nsplit == 1 ? 1.0f / l_run : 1.0f;
       const float unit_v = kE4m3 ? e8m0_value(static_cast<uint32_t>(v_ref)) : 1.0f;
@@ -680,7 +686,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         const float m = finite_or_zero(__shfl_sync(0xffffffffu, m_run, src)), f = __shfl_sync(0xffffffffu, inv_l, src);
         const int r = t * 128 + (warp & 3) * 32 + src;
         const long long out_row = out_row_of(r);
-        const float4 acc = row_sum_seen<kE4m3>(p, p.pages + p.seq_page0[un.seq], un.head, reinterpret_cast<const uint2*>(p.q + out_row * 16),
+        const float4 acc = row_sum_seen<kE4m3>(p, p.pages + un.page0, un.head, reinterpret_cast<const uint2*>(p.q + out_row * 16),
                                                un.key0, lim, m);
         __syncwarp();  // the row as its thread wrote it; only what is not finite is replaced
         if (nsplit == 1) {

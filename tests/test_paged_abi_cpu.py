@@ -120,7 +120,7 @@ def test_bindings_refuse_host_tensors():
 def plan(L, kind, tiles, heads, ctas, cap=None):
     t = arr(tiles).reshape(-1, 3)
     cap = len(t) * heads + ctas if cap is None else cap
-    units, first, n = np.full((cap + 1, 8), -7, dtype=np.int32), arr(np.zeros(ctas + 1)), c_int32()
+    units, first, n = np.full((cap + 1, 16), -7, dtype=np.int32), arr(np.zeros(ctas + 1)), c_int32()
     st = L.mot_dev_paged_plan(kind, t.ctypes.data, len(t), heads, ctas, units.ctypes.data, cap, first.ctypes.data, byref(n))
     assert (units[cap] == -7).all()
     return st, units[: n.value], first
@@ -139,7 +139,7 @@ def test_plan_covers_every_key_once(L, kind, granule, ctas, seed):
     assert first[0] == 0 and first[-1] == len(units) and (np.diff(first) >= 0).all()
     seen, slots, counters = {}, set(), {}
     for u in units:
-        seq, head, row0, k0, k1, slot0, split, counter = (int(x) for x in u)
+        seq, head, row0, k0, k1, slot0, split, counter = (int(x) for x in u[:8])
         assert row0 == 8 * seq and 0 <= head < heads and k0 % granule == 0 and k0 < k1
         number, of = split & 0xFFFF, split >> 16
         seen.setdefault((seq, head), []).append((number, of, k0, k1, slot0, counter))
