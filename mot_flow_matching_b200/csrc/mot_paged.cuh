@@ -281,13 +281,14 @@ mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cfg->kv_dtype == MOT_PAGED_E4M3;
   set_smem_attr(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, TileSmem::bytes(e4m3));
-  const uint32_t small_smem = e4m3 ? SmallSmem<true>::kBytes : SmallSmem<false>::kBytes;
+  const uint32_t small_smem = e4m3 ? SmallShape<true>::kBytes : SmallShape<false>::kBytes;
   set_smem_attr(e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>, small_smem);
   int per_sm = 0;
   bool ok = cudaGetDevice(&h->device) == cudaSuccess &&
             cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) == cudaSuccess &&
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>,
-                                                          kSmallWarps * 32, small_smem) == cudaSuccess &&
+                                                          e4m3 ? SmallShape<true>::kThreads : SmallShape<false>::kThreads, small_smem) ==
+                cudaSuccess &&
             per_sm > 0 && encode_ready() && cudaMalloc(&h->gains, 256 * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&h->rope, static_cast<size_t>(cfg->max_positions) * 64 * sizeof(float2)) == cudaSuccess &&
             cudaMalloc(&h->status, sizeof(int)) == cudaSuccess;
@@ -577,14 +578,15 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
     p.part = static_cast<float*>(workspace) + (i ? static_cast<size_t>(h->ctas[0]) * 2 * kSmallSlot : 0);
     const uint64_t rows = static_cast<uint64_t>(pool->n_pages) * c.n_kv_heads * c.page_size;
     CUtensorMap &km = i ? tp.k_map : small.k_map, &vm = i ? tp.v_map : small.v_map;
-    const uint32_t box = i ? c.page_size : 16;
+    const uint32_t box = i ? c.page_size : std::min(c.page_size, e4m3 ? SmallShape<true>::kKeys : SmallShape<false>::kKeys);
     if (e4m3 ? !map_bytes(&km, pool->k, rows, box, i == 0) || !map_bytes(&vm, pool->v, rows, box, i == 0)
              : !map2d(&km, pool->k, true, 128, rows, 128, box) || !map2d(&vm, pool->v, true, 128, rows, 128, box))
       return MOT_ERR_CUDA;
     if (i == 0) {
       small.a = p;
-      e = e4m3 ? launch_pdl(paged_attn_small_kernel<true>, dim3(h->ctas[0]), dim3(kSmallWarps * 32), SmallSmem<true>::kBytes, st, small)
-               : launch_pdl(paged_attn_small_kernel<false>, dim3(h->ctas[0]), dim3(kSmallWarps * 32), SmallSmem<false>::kBytes, st, small);
+      e = launch_pdl(e4m3 ? paged_attn_small_kernel<true> : paged_attn_small_kernel<false>, dim3(h->ctas[0]),
+                     dim3(e4m3 ? SmallShape<true>::kThreads : SmallShape<false>::kThreads),
+                     e4m3 ? SmallShape<true>::kBytes : SmallShape<false>::kBytes, st, small);
     } else {
       // a tile's 128 rows are whole tokens where the group divides 128: one box
       tp.q_tma = 128 % p.group == 0;

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include "ptx.cuh"
 
@@ -38,6 +39,21 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
   return r;
+}
+
+// four e4m3 -> two f16 pairs, exact
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// untiled bulk copy: addresses and size multiples of 16 bytes
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& w, float (&f)[8]) {
@@ -365,254 +381,221 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return y;
 }
 
-constexpr int kSmallRows = 8;     // query rows of a unit
-constexpr int kSmallWarps = 8;
+// Eight-row matrices of 16-byte rows in the operand layout of mma.sync, four at
+// a time; lane i gives the address of row i % 8 of matrix i / 8.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+constexpr int kSmallRows = 8;  // query rows of a unit
 constexpr int kSmallSlot = kSmallRows * 128 + kSmallRows * 2;  // floats of a partial
 
 struct PagedSmallParams {
-  CUtensorMap k_map, v_map;  // 2D rows of the pool, box of 16 rows x 128 bytes, 128-byte swizzle
+  // 2D rows of the pool; bf16: box {64, rows}, e4m3: bytes, box {128, rows}; 128-byte swizzle; rows = min(page, stage)
+  CUtensorMap k_map, v_map;
   PagedAttnParams a;
 };
 
-// Per warp a ring of pieces, each the keys or the values of 16 tokens: 12 KB in
-// flight a warp, 192 KB an SM, whatever the type.
+// A warp takes 16 keys of a stage; two CTAs an SM, three stages of 32 KB of keys
+// and values each: 192 KB in flight an SM.
 template <bool kE4m3>
-struct SmallSmem {
-  static constexpr int kPieceBytes = kE4m3 ? 2048 : 4096;
-  static constexpr int kPieces = kE4m3 ? 6 : 3;
-  static constexpr uint32_t kRing = kSmallWarps * kPieces * kPieceBytes;
-  static constexpr uint32_t kBytes = kRing + 1024;
+struct SmallShape {
+  static constexpr int kWarps = kE4m3 ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kKeys = 16 * kWarps;
+  static constexpr int kStages = 3;
+  static constexpr uint32_t kHalf = 16384;  // keys, then values
+  static constexpr uint32_t kLine = kKeys * 128;  // bf16: dims 0-63 of all rows, then dims 64-127
+  static constexpr uint32_t kScale = kStages * 2 * kHalf;  // e4m3: [stage][keys, values][128] bytes
+  static constexpr uint32_t kBytes = kScale + (kE4m3 ? kStages * 256 : 0) + 1024;
 };
 
-// 16 keys' registers: keys as the A operand of S^T = K Q^T (lane (g, c) =
-// (lane / 4, lane % 4) holds keys g and g + 8), values as the A operand of
-// O^T += V^T P^T (keys 2c, 2c+1, 2c+8, 2c+9). The rows lie in shared memory in
-// 128-byte lines whose 16-byte pieces are permuted by row & 7. The dims each
-// register pair stands for are permuted so that every lane reads whole pieces
-// and eight lanes hit all banks once: keys, pieces 2c, 2c+1 (and those of the
-// second line); values, piece g. The same permutation is applied to Q, and the
-// permuted rows of O^T are consecutive dims of a lane.
-template <bool kE4m3>
-struct KvGroup;
+// Values that only some of the tile's rows see: an infinity or NaN times a zero
+// weight would reach the rows that do not see it, so it is taken out (set to
+// zero) and its key remembered per dim; rows whose limit is past that key get NaN
+// at the end. Values behind the last key are whatever the page holds there, and
+// become zero.
+struct Unseen {
+  int live;   // keys of the 16 that the unit uses
+  int key0;   // position of the first
+  bool some;  // the rows differ in what they see
+  int* poison;
 
-template <>
-struct KvGroup<false> {  // two lines a row: dims 0-63 of the 16 rows, then dims 64-127
-  uint4 k[2][4];
-  uint4 v[4][2];
-  __device__ __forceinline__ void read_k(const uint8_t* s, int g, int c) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
+  // a bf16 pair: the values of keys k and k + 1 (of the 16) in dim d
+  __device__ __forceinline__ uint32_t bf16_pair(uint32_t w, int k, int d) const {
+    if (k >= live) return 0u;
+    if (k + 1 >= live) w &= 0xffffu;
+    if (some) {
+      if ((w & 0x7f80u) == 0x7f80u) {
+        atomicMin(poison + d, key0 + k);
+        w &= 0xffff0000u;
+      }
+      if ((w & 0x7f800000u) == 0x7f800000u) {
+        atomicMin(poison + d, key0 + k + 1);
+        w &= 0xffffu;
+      }
+    }
+    return w;
+  }
+  // four e4m3: key k, dims d..d + 3
+  __device__ __forceinline__ uint32_t e4m3_quad(uint32_t w, int k, int d) const {
+    if (k >= live) return 0u;
+    if (some) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        k[r][i] = *reinterpret_cast<const uint4*>(s + (i >> 1) * 2048 + (g + 8 * r) * 128 + (((2 * c + (i & 1)) ^ g) << 4));
-  }
-  __device__ __forceinline__ void read_v(const uint8_t* s, int g, int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 2 * c + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        v[i][j] = *reinterpret_cast<const uint4*>(s + j * 2048 + row * 128 + ((g ^ (row & 7)) << 4));
-    }
-  }
-};
-
-template <>
-struct KvGroup<true> {
-  uint4 k[2][2];
-  uint4 v[4];
-  uint32_t ks[2], vs[2];  // scale bytes of keys g, g + 8
-  __device__ __forceinline__ void read_k(const uint8_t* s, int g, int c) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        k[r][i] = *reinterpret_cast<const uint4*>(s + (g + 8 * r) * 128 + (((2 * c + i) ^ g) << 4));
-  }
-  __device__ __forceinline__ void read_v(const uint8_t* s, int g, int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 2 * c + (i & 1) + 8 * (i >> 1);
-      v[i] = *reinterpret_cast<const uint4*>(s + row * 128 + ((g ^ (row & 7)) << 4));
-    }
-  }
-};
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ void set_word(uint4& v, int i, uint32_t w) {
-  if (i == 0) v.x = w;
-  else if (i == 1) v.y = w;
-  else if (i == 2) v.z = w;
-  else v.w = w;
-}
-
-// Values of a group that only some of the tile's rows see: an infinity or NaN
-// times a zero weight would reach the rows that do not see it, so it is taken
-// out (set to zero) and its key remembered per dim; rows whose limit is past
-// that key get NaN at the end.
-template <bool kE4m3>
-__device__ __forceinline__ void take_out_poison(KvGroup<kE4m3>& kv, int* poison, int key0, int g, int c) {
-  if constexpr (!kE4m3) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w = word(kv.v[s][j], i);
-          const int key = key0 + 2 * c + (s & 1) + 8 * (s >> 1);
-          const int dim = 64 * j + 8 * g + 2 * i;
-          if ((w & 0x7f80u) == 0x7f80u) {
-            atomicMin(poison + dim, key);
-            w &= 0xffff0000u;
-          }
-          if ((w & 0x7f800000u) == 0x7f800000u) {
-            atomicMin(poison + dim + 1, key);
-            w &= 0xffffu;
-          }
-          set_word(kv.v[s][j], i, w);
+        if (((w >> (8 * i)) & 0x7fu) == 0x7fu) {
+          atomicMin(poison + d + i, key0 + k);
+          w &= ~(0xffu << (8 * i));
         }
-  } else {
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (kv.vs[r] == 255u) {
-#pragma unroll 1
-        for (int d = 0; d < 32; ++d) atomicMin(poison + 32 * c + d, key0 + g + 8 * r);
-        kv.vs[r] = 0u;
-      }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w = word(kv.v[s], i);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (((w >> (8 * b)) & 0x7fu) == 0x7fu) {
-            atomicMin(poison + 16 * g + 4 * i + b, key0 + 2 * c + (s & 1) + 8 * (s >> 1));
-            w &= ~(0xffu << (8 * b));
-          }
-        set_word(kv.v[s], i, w);
-      }
-  }
-}
-
-// keys at or behind `live` (counted from the group's first): their values are
-// whatever the page holds there, and become zero
-template <bool kE4m3>
-__device__ __forceinline__ void clear_tail(KvGroup<kE4m3>& kv, int live, int g, int c) {
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-    if (2 * c + (s & 1) + 8 * (s >> 1) >= live) {
-      if constexpr (kE4m3)
-        kv.v[s] = make_uint4(0, 0, 0, 0);
-      else
-        kv.v[s][0] = kv.v[s][1] = make_uint4(0, 0, 0, 0);
     }
-  if constexpr (kE4m3)
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (g + 8 * r >= live) kv.vs[r] = 0u;
-}
+    return w;
+  }
+  // a value scale: key k; `part` of 4 of the dims
+  __device__ __forceinline__ uint32_t scale(uint32_t b, int k, int part) const {
+    if (k >= live) return 0u;
+    if (some && b == 255u) {
+#pragma unroll 1
+      for (int d = 0; d < 32; ++d) atomicMin(poison + 32 * part + d, key0 + k);
+      return 0u;
+    }
+    return b;
+  }
+};
 
 // Attention of up to 8 query rows per unit over a range of keys; bound by the
-// bytes of the pages. Each warp streams its own keys, 16 at a time, through its
-// own ring in shared memory (TMA, one barrier a piece, nothing shared between
-// the warps in the loop) and keeps its own running max, sum and O^T; the warps'
-// results are merged through shared memory, the ranges' results by whichever CTA
-// arrives last, in the order of the ranges.
+// bytes of the pages. Each warp takes 16 keys of every stage and keeps its own
+// running max, sum and O^T; the warps' results are merged through shared memory
+// (over the unit's last stage, while the next unit's first stages are on their
+// way), the ranges' results by whichever CTA arrives last, in the order of the
+// ranges. Warp 0 also fetches the pages by TMA, two stages ahead (a warp of its
+// own for that costs the others registers, and they spill).
 // Tensor-core shapes: S^T (16 keys x 8 rows) = K Q^T and O^T (128 dims x 8
 // rows) += V^T P^T, so the keys and values are the 16-row operand and no row is
 // wasted on padding to 16 query rows; P^T gets into operand layout by
-// movmatrix. bf16 pages: P is split into two bf16 (hi + lo), whose products sum
-// in f32, so that the weights are not rounded to 8 bits. e4m3 pages: keys and
-// values become f16 exactly, the scales are applied in f32 to the scores and to
-// the weights (relative to the largest value scale so far, so that a weight in
-// f16 neither overflows nor loses the keys that count); queries are scaled by a
-// power of two into f16.
+// movmatrix. bf16 pages: operands by ldmatrix; P is split into two bf16 (hi +
+// lo), whose products sum in f32, so that the weights are not rounded to 8 bits.
+// e4m3 pages: keys and values become f16 exactly (mma.sync on e4m3 is no way
+// out: on sm_100 it runs as conversions and f16 products); the dims that each
+// register pair stands for are permuted so that a lane reads whole 16-byte
+// pieces, Q alike, and the rows of O^T are consecutive dims of a lane. The
+// scales are applied in f32 to the scores and to the weights (relative to the
+// largest value scale so far, so that a weight in f16 neither overflows nor
+// loses the keys that count); queries are scaled by a power of two into f16.
 // The batch's tables are written by copies, never by a kernel, so they are read
 // before the grid this one depends on has completed.
 template <bool kE4m3>
-__global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
-  using SM = SmallSmem<kE4m3>;
+__global__ void __launch_bounds__(SmallShape<kE4m3>::kThreads, 2)
+paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
+  using SM = SmallShape<kE4m3>;
   const PagedAttnParams& p = sp.a;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float2 s_ml[kSmallWarps][kSmallRows];
+  __shared__ float2 s_ml[SM::kWarps][kSmallRows];
   __shared__ int s_poison[128];
   __shared__ int s_last;
   __shared__ uint32_t s_abort;
-  __shared__ uint64_t s_bar[kSmallWarps][SM::kPieces];
+  __shared__ uint64_t s_full[SM::kStages], s_empty[SM::kStages];
   grid_dep_launch();
   const int warp = warp_id(), lane = lane_id(), g = lane >> 2, c = lane & 3;
-  uint8_t* rings = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ring = rings + warp * (SM::kPieces * SM::kPieceBytes);
-  // a warp's sums for the merge lie in its ring, which is idle by then: [8 rows][132]
-  auto sums = [&](int w, int r) { return reinterpret_cast<float*>(rings + w * (SM::kPieces * SM::kPieceBytes)) + r * 132; };
-  uint64_t* bars = s_bar[warp];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int u_begin = p.cta_unit0[blockIdx.x], u_end = p.cta_unit0[blockIdx.x + 1];
-  if (lane == 0) {
+  if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < SM::kPieces; ++i) mbar_init(&bars[i], 1);
-    if (warp == 0) s_abort = 0u;
+    for (int i = 0; i < SM::kStages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], SM::kWarps);
+    }
+    s_abort = 0u;
     fence_mbar_init();
   }
   __syncthreads();
   const WaitGuard wg{&s_abort, p.status};
-  int slot = 0;        // ring position of the next piece to be read
-  uint32_t phase = 0;  // and its phase
+  // warp 0: the stage to be fetched next is that of unit f_unit at f_key; lane i takes box i
+  const int ps = min(1 << p.page_shift, SM::kKeys), page_mask = (1 << p.page_shift) - 1;
+  int f_unit = u_begin, f_key = -1, f_stage = 0;
+  uint32_t f_phase = 1u;
+  auto fetch = [&] {
+    if (warp != 0 || f_unit >= u_end) return;
+    const PagedUnit* un = p.units + f_unit;
+    if (f_key < 0) f_key = un->key0;
+    const int key1 = un->key1;
+    const int boxes = (min(SM::kKeys, key1 - f_key) + ps - 1) / ps;
+    const int k = f_key + lane * ps;
+    int row = 0;
+    if (lane < boxes) row = ((p.pages[un->page0 + (k >> p.page_shift)] * p.Hkv + un->head) << p.page_shift) + (k & page_mask);
+    mbar_wait(&s_empty[f_stage], f_phase, wg);
+    if (lane == 0) mbar_expect_tx(&s_full[f_stage], static_cast<uint32_t>(boxes * ps) * (kE4m3 ? 258u : 512u));
+    __syncwarp();
+    if (lane < boxes) {
+      uint8_t* dst = stages + f_stage * 2 * SM::kHalf + lane * ps * 128;
+      tma_load_2d(dst, &sp.k_map, &s_full[f_stage], 0, row);
+      tma_load_2d(dst + SM::kHalf, &sp.v_map, &s_full[f_stage], 0, row);
+      if constexpr (kE4m3) {
+        uint8_t* sc = stages + SM::kScale + f_stage * 256 + lane * ps;
+        bulk_load(sc, p.pool.ks + row, ps, &s_full[f_stage]);
+        bulk_load(sc + 128, p.pool.vs + row, ps, &s_full[f_stage]);
+      } else {
+        tma_load_2d(dst + SM::kLine, &sp.k_map, &s_full[f_stage], 64, row);
+        tma_load_2d(dst + SM::kHalf + SM::kLine, &sp.v_map, &s_full[f_stage], 64, row);
+      }
+    }
+    f_key += SM::kKeys;
+    if (f_key >= key1) {
+      ++f_unit;
+      f_key = -1;
+    }
+    if (++f_stage == SM::kStages) {
+      f_stage = 0;
+      f_phase ^= 1u;
+    }
+  };
+  int stage = 0;
+  uint32_t phase = 0;
+  auto advance = [&] {
+    if (++stage == SM::kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
+
+  const int key_w = 16 * warp;  // this warp's keys of a stage
+  grid_dep_wait();
+  // every stage but one is fetched ahead; the one more follows where a stage has been read
+  for (int i = 0; i + 1 < SM::kStages; ++i) fetch();
   for (int u = u_begin; u < u_end; ++u) {
     const PagedUnit un = p.units[u];
     const int rows = min(kSmallRows, un.rows - un.row0);
     auto limit_of = [&](int r) { return max(un.vis, un.past + (un.row0 + min(r, rows - 1)) / p.group + 1); };
     const int lim_min = limit_of(0), lim_max = limit_of(rows - 1);
-    // this warp's groups of 16 keys: un.key0 + 16 warp + 128 n; lane i looks up the pool row of group n0 + i
-    const int key0 = un.key0 + 16 * warp;
-    const int groups = max(0, (un.key1 - key0 + 16 * kSmallWarps - 1) / (16 * kSmallWarps));
-    auto row_at = [&](int n) {
-      const int key = key0 + min(n, groups - 1) * (16 * kSmallWarps);
-      return ((p.pages[un.page0 + (key >> p.page_shift)] * p.Hkv + un.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-    };
-    int rows_now = groups > 0 ? row_at(lane) : 0, rows_next = groups > 32 ? row_at(32 + lane) : 0;
-    if (lim_max != lim_min)
-      for (int i = threadIdx.x; i < 128; i += kSmallWarps * 32) s_poison[i] = INT_MAX;
-    if (u == u_begin) grid_dep_wait();
-    // pieces are numbered keys 0, values 0, keys 1, ...; piece i goes to ring position (slot now + i) % kPieces
-    auto load_piece = [&](int i, int n_base, int at) {
-      const int n = (i >> 1) - n_base;
-      const int row = __shfl_sync(0xffffffffu, n < 32 ? rows_now : rows_next, n & 31);
-      if (lane == 0) {
-        uint8_t* dst = ring + at * SM::kPieceBytes;
-        const CUtensorMap* map = (i & 1) ? &sp.v_map : &sp.k_map;
-        mbar_expect_tx(&bars[at], SM::kPieceBytes);
-        tma_load_2d(dst, map, &bars[at], 0, row);
-        if (!kE4m3) tma_load_2d(dst + 2048, map, &bars[at], 64, row);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < SM::kPieces; ++i)
-      if (i < 2 * groups) load_piece(i, 0, slot + i < SM::kPieces ? slot + i : slot + i - SM::kPieces);
 
-    // this lane's piece of query row g, in the dims order of the key registers
+    // query row g as the B operand. bf16: words 2s, 2s + 1 hold dims 16s + 2c, + 1 and 16s + 8 + 2c, + 1; e4m3 (as f16):
+    // dims 32c + 2i, + 1 in word i
     uint32_t q[16];
     float qf[2] = {p.scale_log2, p.scale_log2};  // score factor of rows 2c, 2c + 1
     {
       const int rr = un.row0 + g;
       const bool live = g < rows;
       const uint4* src = p.q + (static_cast<long long>(un.q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group) * 16;
-      uint4 w[4];
+      if constexpr (!kE4m3) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int piece = kE4m3 ? 4 * c + i : 8 * (i >> 1) + 2 * c + (i & 1);
-        w[i] = live ? __ldg(src + piece) : make_uint4(0, 0, 0, 0);
-      }
-      if (!kE4m3) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = word(w[i >> 2], i & 3);
+        for (int i = 0; i < 16; ++i) q[i] = live ? __ldg(reinterpret_cast<const uint32_t*>(src) + 4 * i + c) : 0u;
       } else {
         float f[4][8];
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          unpack_bf16x8(w[i], f[i]);
+          const uint4 w = live ? __ldg(src + 4 * c + i) : make_uint4(0, 0, 0, 0);
+          unpack_bf16x8(w, f[i]);
           m = fmax3_nan(m, amax8(f[i]), 0.f);
         }
         m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.f);
@@ -628,6 +611,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
         qf[1] *= __shfl_sync(0xffffffffu, up, 8 * c + 4);
       }
     }
+    if (lim_max != lim_min) {
+      for (int i = threadIdx.x; i < 128; i += SM::kWarps * 32) s_poison[i] = INT_MAX;
+      named_bar_sync(1, SM::kWarps * 32);
+    }
 
     float o[8][4];
 #pragma unroll
@@ -636,203 +623,225 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
       for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     int v_ref = 0;  // largest value scale byte so far (e4m3)
-    uint32_t scales = 0;  // bytes: key scales of keys g, g + 8, value scales of the same (e4m3)
-    auto scales_of = [&](int n, int n_base) {
-      const int row = __shfl_sync(0xffffffffu, n - n_base < 32 ? rows_now : rows_next, (n - n_base) & 31) + g;
-      return static_cast<uint32_t>(__ldg(p.pool.ks + row)) | static_cast<uint32_t>(__ldg(p.pool.ks + row + 8)) << 8 |
-             static_cast<uint32_t>(__ldg(p.pool.vs + row)) << 16 | static_cast<uint32_t>(__ldg(p.pool.vs + row + 8)) << 24;
-    };
-    if (kE4m3 && groups > 0) scales = scales_of(0, 0);
 
-    if (lim_max != lim_min) __syncthreads();  // s_poison
-    int n_base = 0;  // rows_now holds groups n_base.., rows_next those 32 behind
-    for (int n = 0; n < groups; ++n) {
-      const int key = key0 + n * (16 * kSmallWarps);
-      if (n - n_base == 32) {
-        n_base = n;
-        rows_now = rows_next;
-        rows_next = groups - n > 32 ? row_at(n + 32 + lane) : 0;
-      }
-      KvGroup<kE4m3> kv;
-      const uint32_t sc = scales;
-      mbar_wait(&bars[slot], phase, wg);
-      kv.read_k(ring + slot * SM::kPieceBytes, g, c);
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, x[4];
-      // base-2 scores; x[0], x[1]: key g, rows 2c, 2c + 1; x[2], x[3]: key g + 8
-      if constexpr (!kE4m3) {
+    // the 16 keys from `key` on; kWhole: every row sees all of them (the other case, code of its own, is rare)
+    auto take = [&](int key, auto whole_c) {
+      constexpr bool whole = decltype(whole_c)::value;
+        const uint8_t* kt = stages + stage * 2 * SM::kHalf;
+        const uint32_t k_addr = smem_u32(kt) + key_w * 128;
+        float s[2][4] = {};  // two sums: shorter chains
+        float x[4];          // base-2 scores; x[0], x[1]: key g, rows 2c, 2c + 1; x[2], x[3]: key g + 8
+        uint32_t vs[2] = {0u, 0u};
+        if constexpr (!kE4m3) {
+          // k-step i: rows 0-7 | 8-15 of pieces 2i, then of 2i + 1
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mma_16816<true>(s, kv.k[0][i].x, kv.k[1][i].x, kv.k[0][i].y, kv.k[1][i].y, q[4 * i], q[4 * i + 1]);
-          mma_16816<true>(s, kv.k[0][i].z, kv.k[1][i].z, kv.k[0][i].w, kv.k[1][i].w, q[4 * i + 2], q[4 * i + 3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = s[i] * qf[i & 1];
-      } else {
-        if (n + 1 < groups) scales = scales_of(n + 1, n_base);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const uint32_t a = word(kv.k[0][i], h), b = word(kv.k[1][i], h);
-            mma_16816<false>(s, e4m3x2_f16x2(a), e4m3x2_f16x2(b), e4m3x2_f16x2(a >> 16), e4m3x2_f16x2(b >> 16),
-                             q[8 * i + 2 * h], q[8 * i + 2 * h + 1]);
+          for (int i = 0; i < 8; ++i) {
+            uint32_t a[4];
+            ldmatrix4(a, k_addr + (i >> 2) * SM::kLine + (lane & 15) * 128 + (((2 * (i & 3) + (lane >> 4)) ^ (lane & 7)) << 4));
+            mma_16816<true>(s[i & 1], a[0], a[1], a[2], a[3], q[2 * i], q[2 * i + 1]);
           }
-        const float kf[2] = {e8m0_value(sc & 255u), e8m0_value((sc >> 8) & 255u)};
-        kv.vs[0] = (sc >> 16) & 255u;
-        kv.vs[1] = sc >> 24;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = s[i] * (qf[i & 1] * kf[i >> 1]);
-      }
-      __syncwarp();
-      if (2 * n + SM::kPieces < 2 * groups) load_piece(2 * n + SM::kPieces, n_base, slot);
-      if (++slot == SM::kPieces) {
-        slot = 0;
-        phase ^= 1u;
-      }
-      mbar_wait(&bars[slot], phase, wg);
-      kv.read_v(ring + slot * SM::kPieceBytes, g, c);
-      if (key + 16 > lim_min) {
-        const int lim0 = limit_of(2 * c), lim1 = limit_of(2 * c + 1);
+          for (int i = 0; i < 4; ++i) x[i] = (s[0][i] + s[1][i]) * qf[i & 1];
+        } else {
+          const uint8_t* sc = stages + SM::kScale + stage * 256 + key_w + g;
+          const float kf[2] = {e8m0_value(sc[0]), e8m0_value(sc[8])};
+          vs[0] = sc[128];
+          vs[1] = sc[136];
+          const uint8_t* kr = kt + (key_w + g) * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (key + g + 8 * (i >> 1) >= ((i & 1) ? lim1 : lim0)) x[i] = -INFINITY;
-        clear_tail<kE4m3>(kv, lim_max - key, g, c);
-        if (lim_max != lim_min) take_out_poison<kE4m3>(kv, s_poison, key, g, c);
-      }
-      // the running max moves only when a score passes it by 2^8
-      const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
-      bool grow = mx0 > m_run[0] + kLazyRescaleLog2 || mx1 > m_run[1] + kLazyRescaleLog2;
-      int v_max = 0;
-      if constexpr (kE4m3) {
-        v_max = static_cast<int>(max(kv.vs[0], kv.vs[1]));
-        grow = grow || v_max > v_ref;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-        float a[2] = {mx0, mx1}, f[2];
+          for (int i = 0; i < 2; ++i) {
+            const uint4 ka = *reinterpret_cast<const uint4*>(kr + (((2 * c + i) ^ g) << 4));
+            const uint4 kb = *reinterpret_cast<const uint4*>(kr + 1024 + (((2 * c + i) ^ g) << 4));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], d));
-          a[i] = fmaxf(a[i], m_run[i]);
-          f[i] = ex2_approx(m_run[i] - finite_or_zero(a[i]));
-          m_run[i] = a[i];
-          l_run[i] *= f[i];
-        }
-        if constexpr (kE4m3) {
-          v_max = max(v_ref, __reduce_max_sync(0xffffffffu, v_max));
-          const float d = ex2_approx(static_cast<float>(v_ref - v_max));
-          f[0] *= d;
-          f[1] *= d;
-          v_ref = v_max;
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[t][i] *= f[i & 1];
-      }
-      const float m0 = finite_or_zero(m_run[0]), m1 = finite_or_zero(m_run[1]);
-      float pr[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(x[i] - ((i & 1) ? m1 : m0));
-      l_run[0] += pr[0] + pr[2];
-      l_run[1] += pr[1] + pr[3];
-      if constexpr (!kE4m3) {
-        const uint32_t h0 = pack_bf162(pr[0], pr[1]), h1 = pack_bf162(pr[2], pr[3]);
-        const uint32_t l0 = pack_bf162(pr[0] - __uint_as_float(h0 << 16), pr[1] - __uint_as_float(h0 & 0xffff0000u));
-        const uint32_t l1 = pack_bf162(pr[2] - __uint_as_float(h1 << 16), pr[3] - __uint_as_float(h1 & 0xffff0000u));
-        const uint32_t b0 = transpose_8x8(h0), b1 = transpose_8x8(h1);
-        const uint32_t d0 = transpose_8x8(l0), d1 = transpose_8x8(l1);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const uint32_t sel = (t & 1) ? 0x7632u : 0x5410u;
-          uint32_t a[4];  // dims 8g + t and 64 + 8g + t; keys 2c, 2c+1 and 2c+8, 2c+9
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            a[h] = __byte_perm(word(kv.v[0][h], t >> 1), word(kv.v[1][h], t >> 1), sel);
-            a[2 + h] = __byte_perm(word(kv.v[2][h], t >> 1), word(kv.v[3][h], t >> 1), sel);
-          }
-          mma_16816<true>(o[t], a[0], a[1], a[2], a[3], b0, b1);
-          mma_16816<true>(o[t], a[0], a[1], a[2], a[3], d0, d1);
-        }
-      } else {
-        float w[4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float f = ex2_approx(static_cast<float>(static_cast<int>(kv.vs[r]) - v_ref));
-          w[2 * r] = pr[2 * r] * f;
-          w[2 * r + 1] = pr[2 * r + 1] * f;
-        }
-        const uint32_t b0 = transpose_8x8(pack_half2(w[0], w[1])), b1 = transpose_8x8(pack_half2(w[2], w[3]));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          // word i of the low and of the high half: dims 16g + 4i.. and 16g + 8 + 4i..
-          uint32_t e[2][2][2];  // [dim half][key pair][dims 0,1 | 2,3]: bytes (key a, key b) per dim
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int kp = 0; kp < 2; ++kp) {
-              const uint32_t a = word(kv.v[2 * kp], 2 * h + i), b = word(kv.v[2 * kp + 1], 2 * h + i);
-              e[h][kp][0] = __byte_perm(a, b, 0x5140);
-              e[h][kp][1] = __byte_perm(a, b, 0x7362);
+            for (int h = 0; h < 4; ++h) {
+              uint32_t a0, a1, b0, b1;
+              e4m3x4_f16x4(word(ka, h), a0, a1);
+              e4m3x4_f16x4(word(kb, h), b0, b1);
+              mma_16816<false>(s[h & 1], a0, b0, a1, b1, q[8 * i + 2 * h], q[8 * i + 2 * h + 1]);
             }
+          }
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const int sh = 16 * (d & 1);
-            mma_16816<false>(o[4 * i + d], e4m3x2_f16x2(e[0][0][d >> 1] >> sh), e4m3x2_f16x2(e[1][0][d >> 1] >> sh),
-                             e4m3x2_f16x2(e[0][1][d >> 1] >> sh), e4m3x2_f16x2(e[1][1][d >> 1] >> sh), b0, b1);
+          for (int i = 0; i < 4; ++i) x[i] = (s[0][i] + s[1][i]) * (qf[i & 1] * kf[i >> 1]);
+        }
+        const Unseen unseen{min(lim_max, un.key1) - key, key, lim_max != lim_min, s_poison};
+        if (!whole) {
+          const int lim0 = min(limit_of(2 * c), un.key1), lim1 = min(limit_of(2 * c + 1), un.key1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key + g + 8 * (i >> 1) >= ((i & 1) ? lim1 : lim0)) x[i] = -INFINITY;
+          if constexpr (kE4m3) {
+            vs[0] = unseen.scale(vs[0], g, c);
+            vs[1] = unseen.scale(vs[1], g + 8, c);
           }
         }
-      }
+        // the running max moves only when a score passes it by 2^8
+        const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+        bool grow = mx0 > m_run[0] + kLazyRescaleLog2 || mx1 > m_run[1] + kLazyRescaleLog2;
+        int v_max = 0;
+        if constexpr (kE4m3) {
+          v_max = static_cast<int>(max(vs[0], vs[1]));
+          grow = grow || v_max > v_ref;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          float a[2] = {mx0, mx1}, f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], d));
+            a[i] = fmaxf(a[i], m_run[i]);
+            f[i] = ex2_approx(m_run[i] - finite_or_zero(a[i]));
+            m_run[i] = a[i];
+            l_run[i] *= f[i];
+          }
+          if constexpr (kE4m3) {
+            v_max = max(v_ref, __reduce_max_sync(0xffffffffu, v_max));
+            const float d = ex2_approx(static_cast<float>(v_ref - v_max));
+            f[0] *= d;
+            f[1] *= d;
+            v_ref = v_max;
+          }
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[t][i] *= f[i & 1];
+        }
+        const float m0 = finite_or_zero(m_run[0]), m1 = finite_or_zero(m_run[1]);
+        float pr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(x[i] - ((i & 1) ? m1 : m0));
+        l_run[0] += pr[0] + pr[2];
+        l_run[1] += pr[1] + pr[3];
+        if constexpr (!kE4m3) {
+          const uint32_t h0 = pack_bf162(pr[0], pr[1]), h1 = pack_bf162(pr[2], pr[3]);
+          const uint32_t l0 = pack_bf162(pr[0] - __uint_as_float(h0 << 16), pr[1] - __uint_as_float(h0 & 0xffff0000u));
+          const uint32_t l1 = pack_bf162(pr[2] - __uint_as_float(h1 << 16), pr[3] - __uint_as_float(h1 & 0xffff0000u));
+          const uint32_t b0 = transpose_8x8(h0), b1 = transpose_8x8(h1);
+          const uint32_t d0 = transpose_8x8(l0), d1 = transpose_8x8(l1);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            // keys 0-7 | 8-15 of dims 16t.. (pieces 2t, 2t + 1), transposed: dims 16t + g, + 8; keys 2c, + 1, then + 8
+            uint32_t a[4];
+            ldmatrix4_trans(a, k_addr + SM::kHalf + (t >> 2) * SM::kLine + ((lane & 7) + ((lane >> 4) << 3)) * 128 +
+                                   (((2 * (t & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a[i] = unseen.bf16_pair(a[i], 2 * c + 8 * (i >> 1), 16 * t + g + 8 * (i & 1));
+            }
+            mma_16816<true>(o[t], a[0], a[1], a[2], a[3], b0, b1);
+            mma_16816<true>(o[t], a[0], a[1], a[2], a[3], d0, d1);
+          }
+        } else {
+          float w[4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float f = ex2_approx(static_cast<float>(static_cast<int>(vs[r]) - v_ref));
+            w[2 * r] = pr[2 * r] * f;
+            w[2 * r + 1] = pr[2 * r + 1] * f;
+          }
+          const uint32_t b0 = transpose_8x8(pack_half2(w[0], w[1])), b1 = transpose_8x8(pack_half2(w[2], w[3]));
+          // keys 2c, 2c + 1, 2c + 8, 2c + 9, dims 16g..16g + 15: eight lanes hit all banks once
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+            v[i] = *reinterpret_cast<const uint4*>(kt + SM::kHalf + (key_w + r) * 128 + ((g ^ (r & 7)) << 4));
+            if (!whole)
+              v[i] = make_uint4(unseen.e4m3_quad(v[i].x, r, 16 * g), unseen.e4m3_quad(v[i].y, r, 16 * g + 4),
+                                unseen.e4m3_quad(v[i].z, r, 16 * g + 8), unseen.e4m3_quad(v[i].w, r, 16 * g + 12));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              // dims 16g + 4i + 2d, + 1 (h = 0) and 8 behind (h = 1): bytes (key a, key b) per dim
+              uint32_t e[2][2][2];  // [h][key pair][dim]
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int kp = 0; kp < 2; ++kp)
+                  e4m3x4_f16x4(__byte_perm(word(v[2 * kp], 2 * h + i), word(v[2 * kp + 1], 2 * h + i), d ? 0x7362 : 0x5140),
+                               e[h][kp][0], e[h][kp][1]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma_16816<false>(o[4 * i + 2 * d + k], e[0][0][k], e[1][0][k], e[0][1][k], e[1][1][k], b0, b1);
+            }
+        }
+    };
+    for (int key_s = un.key0;; key_s += SM::kKeys) {
+      const int key = key_s + key_w;
+      const bool more = key_s + SM::kKeys < un.key1;
+      if (key_s > un.key0) fetch();  // over the stage before this one
+      mbar_wait(&s_full[stage], phase, wg);
+      if (key + 16 <= min(lim_min, un.key1))
+        take(key, std::true_type{});
+      else if (key < un.key1)
+        take(key, std::false_type{});
+      if (!more) break;  // the unit's last stage stays this CTA's for the merge
       __syncwarp();
-      if (2 * n + 1 + SM::kPieces < 2 * groups) load_piece(2 * n + 1 + SM::kPieces, n_base, slot);
-      if (++slot == SM::kPieces) {
-        slot = 0;
-        phase ^= 1u;
-      }
+      if (lane == 0) mbar_arrive(&s_empty[stage]);
+      advance();
     }
 
-    // merge of the warps
-    __syncwarp();
+    // Merge of the warps. A warp's sums, f32 [8 rows][128], lie over its own rows of the last stage: rows 0-3 over its
+    // keys (bf16: line 0), rows 4-7 over its values (line 1 of the keys); dims are permuted by the row so that the
+    // warp's stores hit all banks.
+    auto sum_at = [&](int w, int r, int d) {
+      return reinterpret_cast<float*>(stages + stage * 2 * SM::kHalf + (r >> 2) * (kE4m3 ? SM::kHalf : SM::kLine) + w * 2048) +
+             (r & 3) * 128 + (d ^ ((r >> 1) << 3));
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], d);
     }
     const float unscale = kE4m3 ? e8m0_value(static_cast<uint32_t>(v_ref)) : 1.f;
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 2 * c + i;
       if (g == 0) s_ml[warp][r] = make_float2(m_run[i], l_run[i]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float* dst = sums(warp, r) + (kE4m3 ? 16 * g + 8 * j : 64 * j + 8 * g);
+        if constexpr (kE4m3) {
 #pragma unroll
-        for (int t = 0; t < 8; t += 4)
-          *reinterpret_cast<float4*>(dst + t) = make_float4(o[t][2 * j + i] * unscale, o[t + 1][2 * j + i] * unscale,
-                                                            o[t + 2][2 * j + i] * unscale, o[t + 3][2 * j + i] * unscale);
+          for (int t = 0; t < 8; t += 4)
+            *reinterpret_cast<float4*>(sum_at(warp, r, 16 * g + 8 * j + t)) =
+                make_float4(o[t][2 * j + i] * unscale, o[t + 1][2 * j + i] * unscale, o[t + 2][2 * j + i] * unscale,
+                            o[t + 3][2 * j + i] * unscale);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) *sum_at(warp, r, 16 * t + 8 * j + g) = o[t][2 * j + i];
+        }
       }
     }
-    __syncthreads();
+    named_bar_sync(1, SM::kWarps * 32);
     const int nsplit = un.split >> 16, split = un.split & 0xffff;
-    const int r = warp;  // one warp per row
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float w, const float4 v) {
+    auto write_row = [&](int r, float m, float l, const float4& v) {
+      const int rr = un.row0 + r;
+      const long long out_row = static_cast<long long>(un.q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
+      const float inv = 1.0f / l;
+      reinterpret_cast<uint2*>(p.o + out_row * 16)[lane] = make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
+      if (p.lse && lane == 0) p.lse[out_row] = lse_of(m, l);
+    };
+    auto add = [](float4& acc, float w, const float4& v) {
       acc.x = fmaf(v.x, w, acc.x);
       acc.y = fmaf(v.y, w, acc.y);
       acc.z = fmaf(v.z, w, acc.z);
       acc.w = fmaf(v.w, w, acc.w);
     };
-    if (r < rows) {
+#pragma unroll 1
+    for (int r = warp; r < rows; r += SM::kWarps) {  // a warp a row
+      float m = -INFINITY, l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kSmallWarps; ++i) m = fmaxf(m, s_ml[i][r].x);
+      for (int i = 0; i < SM::kWarps; ++i) m = fmaxf(m, s_ml[i][r].x);
       const float m0 = finite_or_zero(m);
 #pragma unroll
-      for (int i = 0; i < kSmallWarps; ++i) {
+      for (int i = 0; i < SM::kWarps; ++i) {
         const float2 ml = s_ml[i][r];
         const float w = ex2_approx(ml.x - m0);
         l = fmaf(ml.y, w, l);
-        add(w, *reinterpret_cast<const float4*>(sums(i, r) + 4 * lane));
+        add(acc, w, *reinterpret_cast<const float4*>(sum_at(i, r, 4 * lane)));
       }
       if (lim_max != lim_min) {
         const int lr = limit_of(r);
@@ -841,15 +850,21 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
         if (s_poison[4 * lane + 2] < lr) acc.z = NAN;
         if (s_poison[4 * lane + 3] < lr) acc.w = NAN;
       }
-    }
-    bool write = r < rows;
-    if (nsplit > 1) {
-      if (r < rows) {
+      if (nsplit == 1) {
+        write_row(r, m, l, acc);
+      } else {
         float* slot = p.part + static_cast<long long>(un.slot0 + split) * kSmallSlot;
         reinterpret_cast<float4*>(slot + r * 128)[lane] = acc;
         if (lane == 0) reinterpret_cast<float2*>(slot + kSmallRows * 128)[r] = make_float2(m, l);
       }
-      __syncthreads();
+    }
+    fence_proxy_async_smem();  // the stage goes back to the TMA
+    named_bar_sync(1, SM::kWarps * 32);
+    if (lane == 0) mbar_arrive(&s_empty[stage]);
+    advance();
+    __syncwarp();
+    fetch();
+    if (nsplit > 1) {
       if (threadIdx.x == 0) {
         // one fence for the CTA's writes, which the barrier put before it; the counter wraps to 0 with the last
         // arrival: ready for the next call
@@ -857,23 +872,24 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
         s_last = atomicInc(reinterpret_cast<unsigned*>(p.counters) + un.counter, nsplit - 1) == nsplit - 1;
         __threadfence();
       }
-      __syncthreads();
-      write = write && s_last;
-      if (write) {
+      named_bar_sync(1, SM::kWarps * 32);
+      const float* slots = p.part + static_cast<long long>(un.slot0) * kSmallSlot;
+      const bool last = s_last;
+      named_bar_sync(1, SM::kWarps * 32);  // read by all before the next unit may write it
+#pragma unroll 1
+      for (int r = last ? warp : rows; r < rows; r += SM::kWarps) {
         // lane i holds the max and sum of range 32 b + i; the sums of eight ranges are in flight at a time
-        const float* slot = p.part + static_cast<long long>(un.slot0) * kSmallSlot;
         auto ml_of = [&](int i) {
-          return i < nsplit ? __ldcg(reinterpret_cast<const float2*>(slot + static_cast<long long>(i) * kSmallSlot + kSmallRows * 128) + r)
+          return i < nsplit ? __ldcg(reinterpret_cast<const float2*>(slots + static_cast<long long>(i) * kSmallSlot + kSmallRows * 128) + r)
                             : make_float2(-INFINITY, 0.f);
         };
         const float2 first = ml_of(lane);
-        m = first.x;
+        float m = first.x, l = 0.f;
         for (int b = 32; b < nsplit; b += 32) m = fmaxf(m, ml_of(b + lane).x);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         const float m0 = finite_or_zero(m);
-        l = 0.f;
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int b = 0; b < nsplit; b += 32) {
           const float2 ml = b == 0 ? first : ml_of(b + lane);
           const float wl = ex2_approx(ml.x - m0);
@@ -886,27 +902,18 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 2) paged_attn_small_kernel(c
             float4 v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              v[k] = __ldcg(reinterpret_cast<const float4*>(slot + static_cast<long long>(b + min(i + k, n - 1)) * kSmallSlot + r * 128) + lane);
+              v[k] = __ldcg(reinterpret_cast<const float4*>(slots + static_cast<long long>(b + min(i + k, n - 1)) * kSmallSlot + r * 128) + lane);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float w = __shfl_sync(0xffffffffu, wl, i + k);
-              if (i + k < n) add(w, v[k]);
+              if (i + k < n) add(acc, w, v[k]);
             }
           }
         }
+        write_row(r, m, l, acc);
       }
     }
-    if (write) {
-      const int rr = un.row0 + r;
-      const long long out_row = static_cast<long long>(un.q0 + rr / p.group) * p.Hq + un.head * p.group + rr % p.group;
-      const float inv = 1.0f / l;
-      reinterpret_cast<uint2*>(p.o + out_row * 16)[lane] = make_uint2(pack_bf162(acc.x * inv, acc.y * inv), pack_bf162(acc.z * inv, acc.w * inv));
-      if (p.lse && lane == 0) p.lse[out_row] = lse_of(m, l);
-    }
-    fence_proxy_async_smem();  // the rings go back to the TMA
-    __syncthreads();
   }
-  if (u_begin == u_end) grid_dep_wait();
 }
 
 }  // namespace mot

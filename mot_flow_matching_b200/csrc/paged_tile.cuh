@@ -81,13 +81,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0u;
 }
 
-// untiled bulk copy: addresses and size multiples of 16 bytes
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // Byte offset of 16-byte piece `piece` (0..15) of row `row` in a 128 x 128 bf16
 // tile: two boxes of 64 dims, 128 bytes a row, pieces permuted by row & 7.
 __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
@@ -103,10 +96,10 @@ __device__ __forceinline__ void e4m3x16_f16(const uint4& x, uint32_t b, uint32_t
   const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
   uint32_t r[8];
 #pragma unroll
+  for (int i = 0; i < 4; ++i) e4m3x4_f16x4(word(x, i), r[2 * i], r[2 * i + 1]);
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
-    const uint32_t h = e4m3x2_f16x2(w >> (16 * (i & 1)));
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), f2);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&r[i]), f2);
     r[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
