@@ -116,48 +116,57 @@ int log2_of(int v) {
 }
 
 // How the attention's tiles -- (sequence, KV head, query rows), each with its
-// own number of keys -- are cut over the CTAs: the CTAs take equal shares of the
-// work in tile order; a tile that straddles a boundary is split there, at a
-// multiple of `granule` keys, and its ranges are merged on the device. Work is
-// counted in granules, a unit's prologue and merge as `unit_cost` of them.
+// own number of keys -- go to the CTAs. Either whole, the longest first, each to
+// the CTA with the least work so far; or cut: the CTAs take equal shares of the
+// work in tile order, a tile that straddles a boundary is split there, at a
+// multiple of `granule` keys, and its ranges are merged on the device. The
+// cheaper by this count of work, in granules: a unit's prologue and epilogue cost
+// `unit`, a range of a split tile `split` more (its partial result and the
+// merge). Measured: few rows, 128 keys of a warp group against a merge of about
+// 2 us; 256 rows, 2 us a key tile, 3 us a unit, 4-5 us more a range.
 struct CutRule {
-  int granule, unit_cost, min_share;
+  int granule, unit, split, min_share;
 };
-constexpr CutRule kCutRules[2] = {{128, 1, 3}, {kTileKeys, 2, 4}};
+constexpr CutRule kCutRules[2] = {{128, 1, 0, 3}, {kTileKeys, 2, 2, 5}};
 
 struct PagedTile {
   int seq, row0, keys;
 };
 
-// One pass with a given share; returns whether it fits. Without `cut` the tiles
-// stay whole. `units` null: only the test.
-bool cut_units(const std::vector<PagedTile>& tiles, int heads, int ctas, long long share, bool cut, const CutRule& rule,
+int granules_of(const PagedTile& t, const CutRule& rule) { return (t.keys + rule.granule - 1) / rule.granule; }
+
+PagedUnit unit_of(const PagedTile& t, int head, int key0, int key1) {
+  return PagedUnit{t.seq, head, t.row0, key0, key1, 0, 1 << 16, 0, 0, 0, 0, 0, 0, {0, 0, 0}};
+}
+
+// Cut into shares of `share`; returns whether that fits. `units` null: only the test.
+bool cut_units(const std::vector<PagedTile>& tiles, int heads, int ctas, long long share, const CutRule& rule,
                PagedUnit* units, int unit_cap, int* cta_unit0, int* n_units) {
   int cta = 0, n = 0, slots = 0, counters = 0;
   long long load = 0;
-  if (cta_unit0) cta_unit0[0] = 0;
+  if (units) cta_unit0[0] = 0;
   for (const PagedTile& tl : tiles) {
-    const int granules = (tl.keys + rule.granule - 1) / rule.granule;
+    const int granules = granules_of(tl, rule);
     for (int head = 0; head < heads; ++head) {
       const int first = n;
       int at = 0;
       while (at < granules) {
-        const long long room = share - load - rule.unit_cost;
-        if (load > 0 && (cut ? room < 1 : room < granules)) {
+        const bool whole = at == 0 && load + rule.unit + granules <= share;
+        const long long room = whole ? granules : share - load - rule.unit - rule.split;
+        if (load > 0 && room < 1) {
           if (++cta >= ctas) return false;
-          if (cta_unit0) cta_unit0[cta] = n;
+          if (units) cta_unit0[cta] = n;
           load = 0;
           continue;
         }
-        const int take = cut ? static_cast<int>(std::min<long long>(std::max<long long>(room, 1), granules - at)) : granules;
+        const int take = static_cast<int>(std::min<long long>(std::max<long long>(room, 1), granules - at));
         if (units) {
           if (n >= unit_cap) return false;
-          units[n] = PagedUnit{tl.seq, head, tl.row0, at * rule.granule, std::min(tl.keys, (at + take) * rule.granule), 0, 0, 0,
-                               0, 0, 0, 0, 0, {0, 0, 0}};
+          units[n] = unit_of(tl, head, at * rule.granule, std::min(tl.keys, (at + take) * rule.granule));
         }
         ++n;
         at += take;
-        load += take + rule.unit_cost;
+        load += take + rule.unit + (whole ? 0 : rule.split);
       }
       const int pieces = n - first;
       if (units)
@@ -172,36 +181,55 @@ bool cut_units(const std::vector<PagedTile>& tiles, int heads, int ctas, long lo
       }
     }
   }
-  if (cta_unit0)
+  if (units) {
     for (int i = cta + 1; i <= ctas; ++i) cta_unit0[i] = n;
-  if (n_units) *n_units = n;
+    *n_units = n;
+  }
   return true;
 }
 
-// The smallest share that fits, whole tiles where that costs at most 1/16 more.
 bool plan_units(const std::vector<PagedTile>& tiles, int heads, int ctas, const CutRule& rule, PagedUnit* units,
                 int unit_cap, int* cta_unit0, int* n_units) {
-  long long total = 0, largest = 0;
-  for (const PagedTile& tl : tiles) {
-    const long long w = (tl.keys + rule.granule - 1) / rule.granule + rule.unit_cost;
-    total += w * heads;
-    largest = std::max(largest, w);
+  long long total = 0;
+  for (const PagedTile& tl : tiles) total += static_cast<long long>(granules_of(tl, rule) + rule.unit) * heads;
+  // smallest share that fits
+  long long lo = std::max<long long>(rule.min_share, (total + ctas - 1) / ctas), hi = lo;
+  while (!cut_units(tiles, heads, ctas, hi, rule, nullptr, 0, nullptr, nullptr)) {
+    lo = hi + 1;
+    hi *= 2;
   }
-  auto smallest = [&](bool cut) {
-    long long lo = std::max<long long>(cut ? rule.min_share : largest, (total + ctas - 1) / ctas);
-    long long hi = std::max(lo, total + 1);
-    while (lo < hi) {
-      const long long mid = lo + (hi - lo) / 2;
-      if (cut_units(tiles, heads, ctas, mid, cut, rule, nullptr, 0, nullptr, nullptr))
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    return lo;
-  };
-  const long long cut_share = smallest(true), whole_share = smallest(false);
-  const bool cut = whole_share > cut_share + cut_share / 16;
-  return cut_units(tiles, heads, ctas, cut ? cut_share : whole_share, cut, rule, units, unit_cap, cta_unit0, n_units);
+  while (lo < hi) {
+    const long long mid = lo + (hi - lo) / 2;
+    if (cut_units(tiles, heads, ctas, mid, rule, nullptr, 0, nullptr, nullptr))
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  // whole tiles, the longest first, to the CTA with the least work so far
+  const int n = static_cast<int>(tiles.size()) * heads;
+  std::vector<int> order(n), owner(n);
+  for (int i = 0; i < n; ++i) order[i] = i;
+  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return tiles[a / heads].keys > tiles[b / heads].keys; });
+  std::priority_queue<std::pair<long long, int>, std::vector<std::pair<long long, int>>, std::greater<>> free_cta;
+  for (int i = 0; i < ctas; ++i) free_cta.push({0, i});
+  long long largest = 0;
+  for (int i : order) {
+    auto [load, cta] = free_cta.top();
+    free_cta.pop();
+    owner[i] = cta;
+    load += granules_of(tiles[i / heads], rule) + rule.unit;
+    largest = std::max(largest, load);
+    free_cta.push({load, cta});
+  }
+  if (lo < largest) return cut_units(tiles, heads, ctas, lo, rule, units, unit_cap, cta_unit0, n_units);
+  if (n > unit_cap) return false;
+  std::fill(cta_unit0, cta_unit0 + ctas + 1, 0);
+  for (int i = 0; i < n; ++i) ++cta_unit0[owner[i] + 1];
+  for (int i = 0; i < ctas; ++i) cta_unit0[i + 1] += cta_unit0[i];
+  std::vector<int> at(cta_unit0, cta_unit0 + ctas);
+  for (int i : order) units[at[owner[i]]++] = unit_of(tiles[i / heads], i % heads, 0, tiles[i / heads].keys);
+  *n_units = n;
+  return true;
 }
 
 bool paged_device_ok(const mot_paged* h) {

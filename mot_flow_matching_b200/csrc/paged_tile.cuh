@@ -36,7 +36,10 @@ namespace mot {
 
 constexpr int kTileRows = 256;  // query rows of a unit
 constexpr int kTileKeys = 128;
-constexpr int kTileSlot = kTileRows * 128 + kTileRows * 2;  // floats of a partial
+// Floats of a partial: 32 groups of 4 dims, each [256 rows][4], so that the
+// threads of a warp, a row each, write and read 512 bytes in a row; then the
+// rows' (max, sum).
+constexpr int kTileSlot = kTileRows * 128 + kTileRows * 2;
 
 struct PagedTileParams {
   // 2D {128, n_pages * Hkv * page_size}; bf16: box {64, page_size}, 128-byte swizzle; e4m3: bytes, box {128, page_size}
@@ -135,6 +138,22 @@ __device__ __forceinline__ void scores_exp32(const uint32_t (&s)[32], uint32_t t
     pk[i >> 1] = kBf16 ? pack_bf162(p0, p1) : pack_half2(p0, p1);
   }
   tmem_st16(taddr, pk);
+}
+
+// 32 dims of an output row times f, as bf16; whole 32-byte sectors where the
+// output is so aligned
+__device__ __forceinline__ void store_row32(uint4* dst, const uint32_t (&r)[32], float f) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack_bf162(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
+  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0u) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      st_global_v8(dst + 2 * i, w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3], w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
 }
 
 // One value of a cached row as f32.
@@ -644,23 +663,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 #pragma unroll
         for (int i = 0; i < 32; ++i) probe = fmaf(__uint_as_float(r[i]), 0.f, probe);
         if (live && nsplit == 1) {
-          uint4* dst = p.o + orow * 16 + c * 4;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(r[8 * i + k]) * inv;
-            dst[i] = pack_bf16x8(f);
-          }
+          store_row32(p.o + orow * 16 + c * 4, r, inv);
         } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(slot + (t * 128 + row) * 128 + c * 32);
+          float4* dst = reinterpret_cast<float4*>(slot) + c * 8 * kTileRows + t * 128 + row;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = kE4m3 ? __float_as_uint(__uint_as_float(r[4 * i + k]) * unit_v) : r[4 * i + k];
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int i = 0; i < 8; ++i)
+            dst[i * kTileRows] = make_float4(__uint_as_float(r[4 * i]) * unit_v, __uint_as_float(r[4 * i + 1]) * unit_v,
+                                             __uint_as_float(r[4 * i + 2]) * unit_v, __uint_as_float(r[4 * i + 3]) * unit_v);
         }
         __syncwarp();
       }
@@ -691,7 +700,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           if ((w.y & 0x7f800000u) == 0x7f800000u) w.y = (w.y & 0xffffu) | (pack_bf162(0.f, acc.w * f) & 0xffff0000u);
           *dst = w;
         } else {
-          float4* dst = reinterpret_cast<float4*>(slot + r * 128) + lane;
+          float4* dst = reinterpret_cast<float4*>(slot) + lane * kTileRows + r;
           float4 w = *dst;
           if (!isfinite(w.x)) w.x = acc.x;
           if (!isfinite(w.y)) w.y = acc.y;
@@ -703,64 +712,56 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       if (nsplit > 1) {
         // the last range to arrive merges all, in the order of the ranges
         const int threads = unit_rows > 128 ? 256 : 128;
-        __threadfence();
         named_bar_sync(1, threads);
         if (threadIdx.x == 0) {
+          // one fence for the writes that the barrier put before it
+          __threadfence();
           *last_flag = atomicInc(reinterpret_cast<unsigned*>(p.counters) + un.counter, nsplit - 1) == nsplit - 1;
           __threadfence();
         }
         named_bar_sync(1, threads);
         const bool last = *last_flag != 0u;
         named_bar_sync(1, threads);  // read by all before the next unit may write it
-        if (last) {
-          // a warp takes 32 rows: lane i the max and sum of row i, then eight rows' sums at a time, the loads of
-          // a range issued together
+        if (last && live) {
           const float* slots = p.part + static_cast<long long>(un.slot0) * kTileSlot;
-          for (int r0 = warp * 32; r0 < unit_rows; r0 += threads) {
-            auto ml_of = [&](int i) {
-              return __ldcg(reinterpret_cast<const float2*>(slots + static_cast<long long>(i) * kTileSlot + kTileRows * 128) + r0 + lane);
-            };
-            float m = -INFINITY, l = 0.f;
+          const int my = t * 128 + row;
+          auto ml_of = [&](int i) {
+            return __ldcg(reinterpret_cast<const float2*>(slots + static_cast<long long>(i) * kTileSlot + kTileRows * 128) + my);
+          };
+          float m = -INFINITY, l = 0.f;
 #pragma unroll 4
-            for (int i = 0; i < nsplit; ++i) m = fmaxf(m, ml_of(i).x);
-            const float m0 = finite_or_zero(m);
+          for (int i = 0; i < nsplit; ++i) m = fmaxf(m, ml_of(i).x);
+          const float m0 = finite_or_zero(m);
 #pragma unroll 4
+          for (int i = 0; i < nsplit; ++i) {
+            const float2 ml = ml_of(i);
+            l = fmaf(ml.y, ex2_approx(ml.x - m0), l);
+          }
+          if (p.lse) p.lse[orow] = lse_of(m, l);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float acc[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 1
             for (int i = 0; i < nsplit; ++i) {
-              const float2 ml = ml_of(i);
-              l = fmaf(ml.y, ex2_approx(ml.x - m0), l);
-            }
-            const float f = 1.0f / l;
-            const long long my_row = out_row_of(min(r0 + lane, unit_rows - 1));
-            if (p.lse && r0 + lane < unit_rows) p.lse[my_row] = lse_of(m, l);
-            for (int rb = 0; rb < 32 && r0 + rb < unit_rows; rb += 8) {
-              float4 acc[8];
+              const float4* src = reinterpret_cast<const float4*>(slots + static_cast<long long>(i) * kTileSlot) + c * 8 * kTileRows + my;
+              float4 v[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-              for (int i = 0; i < nsplit; ++i) {
-                const float4* src = reinterpret_cast<const float4*>(slots + static_cast<long long>(i) * kTileSlot + (r0 + rb) * 128) + lane;
-                float4 v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + k * 32);
-                const float wi = ex2_approx(ml_of(i).x - m0);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float w = __shfl_sync(0xffffffffu, wi, rb + k);
-                  acc[k].x = fmaf(v[k].x, w, acc[k].x);
-                  acc[k].y = fmaf(v[k].y, w, acc[k].y);
-                  acc[k].z = fmaf(v[k].z, w, acc[k].z);
-                  acc[k].w = fmaf(v[k].w, w, acc[k].w);
-                }
-              }
+              for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + k * kTileRows);
+              const float w = ex2_approx(ml_of(i).x - m0);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, rb + k);
-                const long long row_k = __shfl_sync(0xffffffffu, my_row, rb + k);
-                if (r0 + rb + k < unit_rows)
-                  reinterpret_cast<uint2*>(p.o + row_k * 16)[lane] =
-                      make_uint2(pack_bf162(acc[k].x * fk, acc[k].y * fk), pack_bf162(acc[k].z * fk, acc[k].w * fk));
+                acc[4 * k] = fmaf(v[k].x, w, acc[4 * k]);
+                acc[4 * k + 1] = fmaf(v[k].y, w, acc[4 * k + 1]);
+                acc[4 * k + 2] = fmaf(v[k].z, w, acc[4 * k + 2]);
+                acc[4 * k + 3] = fmaf(v[k].w, w, acc[4 * k + 3]);
               }
             }
+            uint32_t r[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[i]);
+            store_row32(p.o + orow * 16 + c * 4, r, 1.0f / l);
           }
         }
       }
