@@ -109,15 +109,18 @@ __device__ __forceinline__ void e4m3x16_f16(const uint4& x, uint32_t b, uint32_t
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// max of 32 scores and m; NaN comes out as NaN
-__device__ __forceinline__ float scores_max32(const uint32_t (&s)[32], float m) {
-  float a = m, b = -INFINITY;
+// max of a row's 128 scores, in four chains; NaN comes out as NaN
+__device__ __forceinline__ float scores_max(const uint32_t (&s)[4][32]) {
+  float m[4];
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    a = fmax3_nan(a, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-    b = fmax3_nan(b, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-  }
-  return fmax3_nan(a, b, -INFINITY);
+  for (int c = 0; c < 4; ++c) m[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+  for (int i = 1; i < 31; i += 2)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m[c] = fmax3_nan(m[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+  m[0] = fmax3_nan(m[0], __uint_as_float(s[0][31]), m[1]);
+  m[2] = fmax3_nan(m[2], __uint_as_float(s[2][31]), m[3]);
+  return fmax3_nan(m[0], m[2], fmax3_nan(__uint_as_float(s[1][31]), __uint_as_float(s[3][31]), -INFINITY));
 }
 
 // p = 2^(s scale - m) of 32 scores as 16 pairs (bf16 or f16) at taddr; adds them to sum.
@@ -237,8 +240,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       mbar_init(&v_full[i], kE4m3 ? 4 : 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 128);
-      mbar_init(&p_full[2 * i + 1], 128);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(v_raw, 1);
@@ -580,9 +583,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             for (int i = 0; i < 32; ++i)
               if (c * 32 + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
         }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx = scores_max32(s[c], mx);
+        const float mx = scores_max(s);
         float scale = p.scale_log2, v_down = 0.f;
         bool v_grow = false;
         if constexpr (kE4m3) {
@@ -633,7 +634,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           for (int c = 2 * half; c < 2 * half + 2; ++c) scores_exp32<!kE4m3>(s[c], tS + c * 16, scale, neg_m, sum);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&p_full[2 * t + half]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         }
         const float tile_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         l_run = kE4m3 ? fmaf(tile_sum, p_up, l_run) : l_run + tile_sum;
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             float acc[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll 1
+#pragma unroll 3
             for (int i = 0; i < nsplit; ++i) {
               const float4* src = reinterpret_cast<const float4*>(slots + static_cast<long long>(i) * kTileSlot) + c * 8 * kTileRows + my;
               float4 v[8];
