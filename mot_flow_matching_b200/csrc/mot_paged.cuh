@@ -29,8 +29,8 @@ namespace {
 // captured call finds them after the batch is set again. [0]: the few-rows
 // attention, [1]: the 256-row one.
 struct PagedTables {
-  size_t counters[2], cta_unit0[2], n_entries, seq_q0, seq_kv, seq_vis, seq_page0, head_words;  // one block, one copy
-  size_t pages, page_seq, tok, units[2], words;
+  size_t counters[2], cta_unit0[2], n_entries, head_words;  // one block, one copy
+  size_t pages, entries, tok, units[2], words;
   int unit_cap[2];
 };
 
@@ -52,13 +52,9 @@ PagedTables paged_tables(const mot_paged_config& c, const int (&ctas)[2]) {
   for (int i = 0; i < 2; ++i) t.counters[i] = take(ctas[i]);
   for (int i = 0; i < 2; ++i) t.cta_unit0[i] = take(ctas[i] + 1);
   t.n_entries = take(1);
-  t.seq_q0 = take(B + 1);
-  t.seq_kv = take(B);
-  t.seq_vis = take(B);
-  t.seq_page0 = take(B + 1);
   t.head_words = off;
   t.pages = take(c.max_pages);
-  t.page_seq = take(c.max_pages);
+  t.entries = take(4 * static_cast<size_t>(c.max_pages));
   t.tok = take(2 * T);
   const size_t seqs = std::min(B, T);
   const size_t tiles[2] = {seqs * (kSmallMaxRows / kSmallRows), T * G / kTileRows + seqs};
@@ -276,16 +272,13 @@ mot_status paged_copy(mot_paged_t h, mot_paged_batch_t bt, void* k, void* v, int
   p.dense[0] = static_cast<uint4*>(k);
   p.dense[1] = static_cast<uint4*>(v);
   p.pool = pool_view(pool);
-  p.pages = bt->dev + bt->t.pages;
-  p.page_seq = bt->dev + bt->t.page_seq;
-  p.seq_page0 = bt->dev + bt->t.seq_page0;
-  p.seq_kv = bt->dev + bt->t.seq_kv;
+  p.entries = reinterpret_cast<const int4*>(bt->dev + bt->t.entries);
   p.n_entries = bt->dev + bt->t.n_entries;
   p.rows = rows;
   p.Hkv = c.n_kv_heads;
   p.page_shift = log2_of(c.page_size);
   const long long items = static_cast<long long>(bt->entries) * c.n_kv_heads * 2 * (c.page_size / 16);
-  const int grid = static_cast<int>(std::min<long long>((items + 7) / 8, 8ll * h->num_sms));
+  const int grid = static_cast<int>(std::min<long long>((items + 7) / 8, 128ll * h->num_sms));
   const bool e4m3 = c.kv_dtype == MOT_PAGED_E4M3;
   auto kern = e4m3 ? (store ? paged_copy_kernel<true, true> : paged_copy_kernel<true, false>)
                    : (store ? paged_copy_kernel<false, true> : paged_copy_kernel<false, false>);
@@ -427,6 +420,10 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
       bt->times.resize(n_pages, 0);
     }
     std::vector<PagedTile> tiles[2];
+    struct Seq {
+      int q0, page0, past, vis;
+    };
+    std::vector<Seq> seqs(batch);
     bt->batch = 0;  // nothing is described until the copies below are enqueued
     ++bt->set_no;
     int* w = bt->host.data();
@@ -436,10 +433,8 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
     for (int b = 0; b < batch; ++b) {
       const int used = (kv_len[b] + c.page_size - 1) >> shift, past = kv_len[b] - q_len[b];
       const int* row = table + static_cast<size_t>(b) * table_stride;
-      w[t.seq_q0 + b] = q0;
-      w[t.seq_page0 + b] = e0;
-      w[t.seq_kv + b] = kv_len[b];
-      w[t.seq_vis + b] = visible ? visible[b] : 0;
+      const int vis = visible ? visible[b] : 0;
+      seqs[b] = Seq{q0, e0, past, vis};
       for (int i = 0; i < used; ++i) {
         const int id = row[i];
         if (bt->stamp[id] != bt->set_no) {
@@ -450,7 +445,11 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
           repeated = true;
         }
         w[t.pages + e0 + i] = id;
-        w[t.page_seq + e0 + i] = b;
+        int* entry = w + t.entries + 4 * (e0 + i);
+        entry[0] = id;
+        entry[1] = b;
+        entry[2] = i << shift;
+        entry[3] = std::min(c.page_size, kv_len[b] - (i << shift));
       }
       for (int i = 0; i < q_len[b]; ++i) {
         const int pos = past + i;
@@ -460,13 +459,11 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
       const int rows = q_len[b] * group, kind = rows <= kSmallMaxRows ? 0 : 1, step = kind ? kTileRows : kSmallRows;
       for (int r = 0; r < rows; r += step) {
         const int last = std::min(rows, r + step) - 1;
-        tiles[kind].push_back(PagedTile{b, r, std::max(w[t.seq_vis + b], past + last / group + 1)});
+        tiles[kind].push_back(PagedTile{b, r, std::max(vis, past + last / group + 1)});
       }
       q0 += q_len[b];
       e0 += used;
     }
-    w[t.seq_q0 + batch] = q0;
-    w[t.seq_page0 + batch] = e0;
     w[t.n_entries] = e0;
     bt->repeated = repeated;
     bt->repeated_written = false;
@@ -483,11 +480,12 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
       PagedUnit* units = reinterpret_cast<PagedUnit*>(w + t.units[i]);
       for (int k = 0; k < n_units[i]; ++k) {
         PagedUnit& un = units[k];
-        un.q0 = w[t.seq_q0 + un.seq];
+        const Seq& sq = seqs[un.seq];
+        un.q0 = sq.q0;
         un.rows = q_len[un.seq] * group;
-        un.past = kv_len[un.seq] - q_len[un.seq];
-        un.vis = w[t.seq_vis + un.seq];
-        un.page0 = w[t.seq_page0 + un.seq];
+        un.past = sq.past;
+        un.vis = sq.vis;
+        un.page0 = sq.page0;
       }
     }
   } catch (...) {
@@ -495,7 +493,7 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
   }
   const size_t pieces[][2] = {{0, t.head_words},
                               {t.pages, static_cast<size_t>(entries)},
-                              {t.page_seq, static_cast<size_t>(entries)},
+                              {t.entries, static_cast<size_t>(4 * entries)},
                               {t.tok, static_cast<size_t>(2 * tokens)},
                               {t.units[0], static_cast<size_t>(n_units[0]) * (sizeof(PagedUnit) / 4)},
                               {t.units[1], static_cast<size_t>(n_units[1]) * (sizeof(PagedUnit) / 4)}};
@@ -543,13 +541,14 @@ mot_status mot_paged_append(mot_paged_t h, mot_paged_batch_t bt, const void* qkv
   p.page_shift = log2_of(c.page_size);
   p.page_mask = c.page_size - 1;
   p.eps = c.rms_eps;
-  const int quads = (c.n_q_heads + 2 * c.n_kv_heads + 3) / 4;  // four heads a warp at a time
-  const long long all = static_cast<long long>(p.T) * quads;
-  p.heads_per_lane = static_cast<int>(std::min<long long>(4, std::max<long long>(1, all / (32ll * h->num_sms))));
-  p.strips = (quads + p.heads_per_lane - 1) / p.heads_per_lane;
+  // four heads a warp at a time, a strip of one or of four such; long strips once they fill the GPU
+  const int quads = (c.n_q_heads + 2 * c.n_kv_heads + 3) / 4;
+  const bool longs = static_cast<long long>(p.T) * quads >= 4 * 32ll * h->num_sms;
+  p.strips = longs ? (quads + 3) / 4 : quads;
   const long long warps = static_cast<long long>(p.T) * p.strips;
-  const int grid = static_cast<int>(std::min<long long>((warps + 7) / 8, 8ll * h->num_sms));
-  auto kern = c.kv_dtype == MOT_PAGED_E4M3 ? paged_append_kernel<true> : paged_append_kernel<false>;
+  const int grid = static_cast<int>(std::min<long long>((warps + 7) / 8, 128ll * h->num_sms));
+  auto kern = c.kv_dtype == MOT_PAGED_E4M3 ? (longs ? paged_append_kernel<true, 4> : paged_append_kernel<true, 1>)
+                                           : (longs ? paged_append_kernel<false, 4> : paged_append_kernel<false, 1>);
   return launch_pdl(kern, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? MOT_OK
                                                                                                           : MOT_ERR_CUDA;
 }

@@ -127,7 +127,7 @@ struct PagedAppendParams {
   const float2* rope;  // [positions, 64]
   const int2* tok;     // per token: position, page
   int T, Hq, Hkv, page_mask, page_shift;
-  int strips, heads_per_lane;  // a token's heads are cut into `strips` strips
+  int strips;  // a token's heads are cut into `strips` strips
   float eps;
 };
 
@@ -135,39 +135,47 @@ struct PagedAppendParams {
 // lanes share a head, lane e holding dims 8e..8e+7 and 64 + 8e..+7, so that the
 // rotate-half pair (j, j + 64) sits in one lane, all loads and stores are 16
 // bytes, the norm is three shuffles, and the eight (cos, sin) pairs of a lane
-// serve all its heads.
-template <bool kE4m3>
+// serve all its heads. A strip's heads (kQuads times four) are all loaded before
+// the first is used. Bound by bytes; few tokens: by the launch, with short strips.
+template <bool kE4m3, int kQuads>
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   grid_dep_launch();
-  grid_dep_wait();
   const int H = p.Hq + 2 * p.Hkv;
   const long long work = static_cast<long long>(p.T) * p.strips;
   const int lane = lane_id(), sub = lane >> 3, e = lane & 7;
-  for (long long w = blockIdx.x * 8ll + warp_id(); w < work; w += gridDim.x * 8ll) {
+  long long w = blockIdx.x * 8ll + warp_id();
+  int2 tok = make_int2(0, 0);
+  if (w < work) tok = p.tok[w / p.strips];  // the batch's tables are written by copies, never by a kernel
+  grid_dep_wait();
+  while (w < work) {
     const int t = static_cast<int>(w / p.strips), strip = static_cast<int>(w % p.strips);
-    const int2 tok = p.tok[t];
+    const int h0 = strip * kQuads * 4 + sub;
+    const uint4* src = p.qkv + (static_cast<long long>(t) * H + h0) * 16 + e;
+    uint4 x[kQuads][2];
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+      if (h0 + 4 * i < H) {
+        x[i][0] = __ldcs(src + 64 * i);
+        x[i][1] = __ldcs(src + 64 * i + 8);
+      }
     float2 cs[8];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float4 r = reinterpret_cast<const float4*>(p.rope + static_cast<long long>(tok.x) * 64 + 8 * e)[i >> 1];
+      const float4 r = __ldg(reinterpret_cast<const float4*>(p.rope + static_cast<long long>(tok.x) * 64 + 8 * e) + (i >> 1));
       cs[i] = make_float2(r.x, r.y);
       cs[i + 1] = make_float2(r.z, r.w);
     }
     const long long page_row = static_cast<long long>(tok.y) * p.Hkv;
     const int off = tok.x & p.page_mask;
-    const int h_begin = strip * p.heads_per_lane * 4;
-    for (int i = 0; i < p.heads_per_lane; ++i) {
-      const int h = h_begin + 4 * i + sub;
+    const long long next = w + gridDim.x * 8ll;
+    if (next < work) tok = p.tok[next / p.strips];
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      const int h = h0 + 4 * i;
       const bool live = h < H;
-      uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-      if (live) {
-        const uint4* src = p.qkv + (static_cast<long long>(t) * H + h) * 16;
-        ra = src[e];
-        rb = src[8 + e];
-      }
       float a[8], b[8];
-      unpack_bf16x8(ra, a);
-      unpack_bf16x8(rb, b);
+      unpack_bf16x8(live ? x[i][0] : make_uint4(0, 0, 0, 0), a);
+      unpack_bf16x8(live ? x[i][1] : make_uint4(0, 0, 0, 0), b);
       const bool is_v = h >= p.Hq + p.Hkv;
       float ss = 0.f;
 #pragma unroll
@@ -176,12 +184,18 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
       for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (!is_v) {
         const float rstd = __frsqrt_rn(ss * (1.0f / 128.0f) + p.eps);
-        const float* gain = p.gains + (h < p.Hq ? 0 : 128) + 8 * e;
+        const float4* gain = reinterpret_cast<const float4*>(p.gains + (h < p.Hq ? 0 : 128) + 8 * e);
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          const float x = a[d] * rstd * gain[d], y = b[d] * rstd * gain[64 + d];
-          a[d] = x * cs[d].x - y * cs[d].y;
-          b[d] = y * cs[d].x + x * cs[d].y;
+        for (int q = 0; q < 2; ++q) {
+          const float4 ga = __ldg(gain + q), gb = __ldg(gain + 16 + q);
+          const float fa[4] = {ga.x, ga.y, ga.z, ga.w}, fb[4] = {gb.x, gb.y, gb.z, gb.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int d = 4 * q + k;
+            const float u = a[d] * rstd * fa[k], v = b[d] * rstd * fb[k];
+            a[d] = u * cs[d].x - v * cs[d].y;
+            b[d] = v * cs[d].x + u * cs[d].y;
+          }
         }
       }
       if (kE4m3) {
@@ -206,10 +220,11 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
           const int g = h - p.Hq - (is_v ? p.Hkv : 0);
           dst = reinterpret_cast<uint4*>((is_v ? p.pool.v : p.pool.k) + (((page_row + g) << p.page_shift) + off) * 256);
         }
-        dst[e] = is_v ? ra : pack_bf16x8(a);
-        dst[8 + e] = is_v ? rb : pack_bf16x8(b);
+        dst[e] = is_v ? x[i][0] : pack_bf16x8(a);
+        dst[8 + e] = is_v ? x[i][1] : pack_bf16x8(b);
       }
     }
+    w = next;
   }
 }
 
@@ -217,10 +232,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
 struct PagedCopyParams {
   uint4* dense[2];  // k, v: bf16 [B, Hkv, rows, 128]
   PagedPool pool;
-  const int* pages;      // page of table entry i (all sequences' entries, one after another)
-  const int* page_seq;   // its sequence
-  const int* seq_page0;  // first entry of a sequence
-  const int* seq_kv;
+  const int4* entries;   // per table entry in use: page, sequence, first token, tokens
   const int* n_entries;  // entries of the batch as it is set now
   int rows, Hkv, page_shift;
 };
@@ -233,21 +245,25 @@ struct PagedCopyParams {
 template <bool kE4m3, bool kStore>
 __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__ PagedCopyParams p) {
   grid_dep_launch();
-  grid_dep_wait();
   const int lane = lane_id(), sub = lane >> 3, e = lane & 7;
   const int runs = 1 << (p.page_shift - 4);
   const long long items = static_cast<long long>(*p.n_entries) * p.Hkv * 2 * runs;
+  bool waited = false;  // the batch's tables are written by copies, never by a kernel: read before the wait
   for (long long w = blockIdx.x * 8ll + warp_id(); w < items; w += gridDim.x * 8ll) {
     const int run = static_cast<int>(w & (runs - 1));
     long long r = w >> (p.page_shift - 4);
     const int kv = static_cast<int>(r & 1);
     r >>= 1;
-    const int head = static_cast<int>(r % p.Hkv), entry = static_cast<int>(r / p.Hkv);
-    const int seq = p.page_seq[entry];
-    const int j0 = ((entry - p.seq_page0[seq]) << p.page_shift) + run * 16;
-    const int live = p.seq_kv[seq] - j0;  // rows of this run that the sequence has
+    const int head = static_cast<int>(r % p.Hkv);
+    const int4 entry = p.entries[r / p.Hkv];
+    const int seq = entry.y, j0 = entry.z + run * 16;
+    const int live = entry.w - run * 16;  // rows of this run that the sequence has
+    if (!waited) {
+      grid_dep_wait();
+      waited = true;
+    }
     if (live <= 0) continue;
-    const long long prow = ((static_cast<long long>(p.pages[entry]) * p.Hkv + head) << p.page_shift) + run * 16;
+    const long long prow = ((static_cast<long long>(entry.x) * p.Hkv + head) << p.page_shift) + run * 16;
     const long long drow = (static_cast<long long>(seq) * p.Hkv + head) * p.rows + j0;
     uint4* dense = p.dense[kv] + drow * 16;
     uint8_t* page = (kv ? p.pool.v : p.pool.k) + prow * (kE4m3 ? 128 : 256);
@@ -312,6 +328,7 @@ __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__
       }
     }
   }
+  if (!waited) grid_dep_wait();
 }
 
 // ---------------------------------------------------------------- attention, few rows
