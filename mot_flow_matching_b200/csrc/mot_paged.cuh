@@ -541,14 +541,18 @@ mot_status mot_paged_append(mot_paged_t h, mot_paged_batch_t bt, const void* qkv
   p.page_shift = log2_of(c.page_size);
   p.page_mask = c.page_size - 1;
   p.eps = c.rms_eps;
-  // four heads a warp at a time, a strip of one or of four such; long strips once they fill the GPU
   const int quads = (c.n_q_heads + 2 * c.n_kv_heads + 3) / 4;
-  const bool longs = static_cast<long long>(p.T) * quads >= 4 * 32ll * h->num_sms;
-  p.strips = longs ? (quads + 3) / 4 : quads;
-  const long long warps = static_cast<long long>(p.T) * p.strips;
-  const int grid = static_cast<int>(std::min<long long>((warps + 7) / 8, 128ll * h->num_sms));
-  auto kern = c.kv_dtype == MOT_PAGED_E4M3 ? (longs ? paged_append_kernel<true, 4> : paged_append_kernel<true, 1>)
-                                           : (longs ? paged_append_kernel<false, 4> : paged_append_kernel<false, 1>);
+  // Four heads a warp while that is one wave of warps (24 an SM); sixteen up to two waves (16 an SM); then a token.
+  // us at 32/8 heads, e4m3, for 64 / 256 / 700 / 1300 / 2368 / 8192 tokens: 2.8 / 3.2 / 7.0 / 11.4 / 20.7 / 71,
+  // 3.7 / 4.4 / 4.8 / 9.1 / 15.0 / 47 and 6.9 / 7.0 / 9.4 / 10.2 / 12.1 / 41.
+  const long long t = p.T;
+  const int mode = t * quads <= 24ll * h->num_sms ? 0 : t * ((quads + 3) / 4) <= 32ll * h->num_sms ? 1 : 2;
+  const int strips = mode == 0 ? quads : mode == 1 ? (quads + 3) / 4 : 1;
+  const int grid = static_cast<int>(std::min<long long>((t * strips + 7) / 8, 128ll * h->num_sms));
+  const bool e4m3 = c.kv_dtype == MOT_PAGED_E4M3;
+  auto kern = mode == 0   ? (e4m3 ? paged_append_kernel<true, 1, false> : paged_append_kernel<false, 1, false>)
+              : mode == 1 ? (e4m3 ? paged_append_kernel<true, 4, false> : paged_append_kernel<false, 4, false>)
+                          : (e4m3 ? paged_append_kernel<true, 4, true> : paged_append_kernel<false, 4, true>);
   return launch_pdl(kern, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? MOT_OK
                                                                                                           : MOT_ERR_CUDA;
 }

@@ -127,101 +127,133 @@ struct PagedAppendParams {
   const float2* rope;  // [positions, 64]
   const int2* tok;     // per token: position, page
   int T, Hq, Hkv, page_mask, page_shift;
-  int strips;  // a token's heads are cut into `strips` strips
   float eps;
 };
 
-// One warp takes one strip of one token's heads, four heads at a time: eight
-// lanes share a head, lane e holding dims 8e..8e+7 and 64 + 8e..+7, so that the
-// rotate-half pair (j, j + 64) sits in one lane, all loads and stores are 16
+// Eight lanes share a head, lane e holding dims 8e..8e+7 and 64 + 8e..+7, so that
+// the rotate-half pair (j, j + 64) sits in one lane, all loads and stores are 16
 // bytes, the norm is three shuffles, and the eight (cos, sin) pairs of a lane
-// serve all its heads. A strip's heads (kQuads times four) are all loaded before
-// the first is used. Bound by bytes; few tokens: by the launch, with short strips.
-template <bool kE4m3, int kQuads>
+// serve all its heads; a warp has four heads at a time, and the loads of kQuads
+// such fours are issued before the first is used. kWhole: a warp takes a whole
+// token, the next fours on their way; else a token is cut into strips of kQuads.
+// Bound by bytes, and by a warp's chain of loads and norms where tokens are few.
+template <bool kE4m3, int kQuads, bool kWhole>
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   grid_dep_launch();
   const int H = p.Hq + 2 * p.Hkv;
-  const long long work = static_cast<long long>(p.T) * p.strips;
+  const int quads = (H + 3) >> 2;
+  const int strips = kWhole ? 1 : (quads + kQuads - 1) / kQuads;  // pieces a token is cut into
+  const long long work = static_cast<long long>(p.T) * strips;
   const int lane = lane_id(), sub = lane >> 3, e = lane & 7;
   long long w = blockIdx.x * 8ll + warp_id();
   int2 tok = make_int2(0, 0);
-  if (w < work) tok = p.tok[w / p.strips];  // the batch's tables are written by copies, never by a kernel
+  if (w < work) tok = p.tok[w / strips];  // the batch's tables are written by copies, never by a kernel
   grid_dep_wait();
   while (w < work) {
-    const int t = static_cast<int>(w / p.strips), strip = static_cast<int>(w % p.strips);
-    const int h0 = strip * kQuads * 4 + sub;
-    const uint4* src = p.qkv + (static_cast<long long>(t) * H + h0) * 16 + e;
-    uint4 x[kQuads][2];
+    const int t = static_cast<int>(w / strips);
+    const int q_begin = kWhole ? 0 : static_cast<int>(w % strips) * kQuads, q_end = kWhole ? quads : q_begin + 1;
+    const uint4* src = p.qkv + (static_cast<long long>(t) * H + sub) * 16 + e;
+    uint4 x[kQuads][2], y[kQuads][2];
+    auto load = [&](uint4 (&v)[kQuads][2], int q0) {
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i)
-      if (h0 + 4 * i < H) {
-        x[i][0] = __ldcs(src + 64 * i);
-        x[i][1] = __ldcs(src + 64 * i + 8);
+      for (int i = 0; i < kQuads; ++i) {
+        v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+        if (4 * (q0 + i) + sub < H) {
+          v[i][0] = __ldcs(src + 64 * (q0 + i));
+          v[i][1] = __ldcs(src + 64 * (q0 + i) + 8);
+        }
       }
-    float2 cs[8];
+    };
+    load(x, q_begin);
+    float cs[8], sn[8];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const float4 r = __ldg(reinterpret_cast<const float4*>(p.rope + static_cast<long long>(tok.x) * 64 + 8 * e) + (i >> 1));
-      cs[i] = make_float2(r.x, r.y);
-      cs[i + 1] = make_float2(r.z, r.w);
+      cs[i] = r.x;
+      sn[i] = r.y;
+      cs[i + 1] = r.z;
+      sn[i + 1] = r.w;
     }
     const long long page_row = static_cast<long long>(tok.y) * p.Hkv;
     const int off = tok.x & p.page_mask;
     const long long next = w + gridDim.x * 8ll;
-    if (next < work) tok = p.tok[next / p.strips];
+    if (next < work) tok = p.tok[next / strips];
+    for (int q0 = q_begin; q0 < q_end; q0 += kQuads) {
+      if (kWhole && q0 + kQuads < q_end) load(y, q0 + kQuads);
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i) {
-      const int h = h0 + 4 * i;
-      const bool live = h < H;
-      float a[8], b[8];
-      unpack_bf16x8(live ? x[i][0] : make_uint4(0, 0, 0, 0), a);
-      unpack_bf16x8(live ? x[i][1] : make_uint4(0, 0, 0, 0), b);
-      const bool is_v = h >= p.Hq + p.Hkv;
-      float ss = 0.f;
+      for (int i = 0; i < kQuads; ++i) {
+        const int h = 4 * (q0 + i) + sub;
+        if (4 * (q0 + i) >= H) break;
+        const bool live = h < H, is_v = h >= p.Hq + p.Hkv;
+        const bool some_qk = 4 * (q0 + i) < p.Hq + p.Hkv, some_kv = 4 * (q0 + i) + 3 >= p.Hq;  // of the warp's four
+        float a[8], b[8];
+        unpack_bf16x8(x[i][0], a);
+        unpack_bf16x8(x[i][1], b);
+        if (some_qk) {
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) ss = fmaf(a[d], a[d], fmaf(b[d], b[d], ss));
+          for (int d = 0; d < 8; d += 2) {
+            ffma2(s0, s1, a[d], a[d + 1], a[d], a[d + 1], s0, s1);
+            ffma2(s0, s1, b[d], b[d + 1], b[d], b[d + 1], s0, s1);
+          }
+          float ss = s0 + s1;
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (!is_v) {
-        const float rstd = __frsqrt_rn(ss * (1.0f / 128.0f) + p.eps);
-        const float4* gain = reinterpret_cast<const float4*>(p.gains + (h < p.Hq ? 0 : 128) + 8 * e);
+          for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (!is_v) {
+            const float rstd = __frsqrt_rn(ss * (1.0f / 128.0f) + p.eps);
+            const float4* gain = reinterpret_cast<const float4*>(p.gains + (h < p.Hq ? 0 : 128) + 8 * e);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 ga = __ldg(gain + q), gb = __ldg(gain + 16 + q);
-          const float fa[4] = {ga.x, ga.y, ga.z, ga.w}, fb[4] = {gb.x, gb.y, gb.z, gb.w};
+            for (int q = 0; q < 2; ++q) {
+              const float4 ga = __ldg(gain + q), gb = __ldg(gain + 16 + q);
+              const float fa[4] = {ga.x, ga.y, ga.z, ga.w}, fb[4] = {gb.x, gb.y, gb.z, gb.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int d = 4 * q + k;
-            const float u = a[d] * rstd * fa[k], v = b[d] * rstd * fb[k];
-            a[d] = u * cs[d].x - v * cs[d].y;
-            b[d] = v * cs[d].x + u * cs[d].y;
+              for (int k = 0; k < 4; k += 2) {
+                const int d = 4 * q + k;
+                float u0, u1, v0, v1, t0, t1;
+                fmul2(u0, u1, a[d], a[d + 1], rstd, rstd);
+                fmul2(v0, v1, b[d], b[d + 1], rstd, rstd);
+                fmul2(u0, u1, u0, u1, fa[k], fa[k + 1]);
+                fmul2(v0, v1, v0, v1, fb[k], fb[k + 1]);
+                fmul2(t0, t1, v0, v1, sn[d], sn[d + 1]);
+                ffma2(a[d], a[d + 1], u0, u1, cs[d], cs[d + 1], -t0, -t1);
+                fmul2(t0, t1, u0, u1, sn[d], sn[d + 1]);
+                ffma2(b[d], b[d + 1], v0, v1, cs[d], cs[d + 1], t0, t1);
+              }
+            }
           }
         }
-      }
-      if (kE4m3) {
-        float m = fmax3_nan(amax8(a), amax8(b), 0.f);
+        if (kE4m3 && some_kv) {
+          float m = fmax3_nan(amax8(a), amax8(b), 0.f);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
-        if (live && h >= p.Hq) {
-          const int g = h - p.Hq - (is_v ? p.Hkv : 0);
-          const long long row = ((page_row + g) << p.page_shift) + off;
-          uint8_t* dst = (is_v ? p.pool.v : p.pool.k) + row * 128;
-          const uint32_t sc = e8m0_of_amax(m);
-          reinterpret_cast<uint2*>(dst)[e] = quant8(a, sc);
-          reinterpret_cast<uint2*>(dst)[8 + e] = quant8(b, sc);
-          if (e == 0) (is_v ? p.pool.vs : p.pool.ks)[row] = static_cast<uint8_t>(sc);
+          for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+          if (live && h >= p.Hq) {
+            const int g = h - p.Hq - (is_v ? p.Hkv : 0);
+            const long long row = ((page_row + g) << p.page_shift) + off;
+            uint8_t* dst = (is_v ? p.pool.v : p.pool.k) + row * 128;
+            const uint32_t sc = e8m0_of_amax(m);
+            reinterpret_cast<uint2*>(dst)[e] = quant8(a, sc);
+            reinterpret_cast<uint2*>(dst)[8 + e] = quant8(b, sc);
+            if (e == 0) (is_v ? p.pool.vs : p.pool.ks)[row] = static_cast<uint8_t>(sc);
+          }
+        }
+        if (live && (!kE4m3 || h < p.Hq)) {
+          uint4* dst;
+          if (h < p.Hq) {
+            dst = p.q + (static_cast<long long>(t) * p.Hq + h) * 16;
+          } else {
+            const int g = h - p.Hq - (is_v ? p.Hkv : 0);
+            dst = reinterpret_cast<uint4*>((is_v ? p.pool.v : p.pool.k) + (((page_row + g) << p.page_shift) + off) * 256);
+          }
+          dst[e] = is_v ? x[i][0] : pack_bf16x8(a);
+          dst[8 + e] = is_v ? x[i][1] : pack_bf16x8(b);
         }
       }
-      if (live && (!kE4m3 || h < p.Hq)) {
-        uint4* dst;
-        if (h < p.Hq) {
-          dst = p.q + (static_cast<long long>(t) * p.Hq + h) * 16;
-        } else {
-          const int g = h - p.Hq - (is_v ? p.Hkv : 0);
-          dst = reinterpret_cast<uint4*>((is_v ? p.pool.v : p.pool.k) + (((page_row + g) << p.page_shift) + off) * 256);
+      if (kWhole) {
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          x[i][0] = y[i][0];
+          x[i][1] = y[i][1];
         }
-        dst[e] = is_v ? x[i][0] : pack_bf16x8(a);
-        dst[8 + e] = is_v ? x[i][1] : pack_bf16x8(b);
       }
     }
     w = next;
