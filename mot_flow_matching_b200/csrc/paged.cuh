@@ -261,6 +261,26 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------------- dense <-> pages
+// 32 bytes of one lane, a whole sector, where the address allows (whole: 32-byte aligned)
+__device__ __forceinline__ void load32(const uint4* src, uint4& a, uint4& b, bool whole) {
+  if (whole) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(src));
+  } else {
+    a = src[0];
+    b = src[1];
+  }
+}
+__device__ __forceinline__ void store32(uint4* dst, const uint4& a, const uint4& b, bool whole) {
+  if (whole) {
+    st_global_v8(dst, a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w);
+  } else {
+    dst[0] = a;
+    dst[1] = b;
+  }
+}
+
 struct PagedCopyParams {
   uint4* dense[2];  // k, v: bf16 [B, Hkv, rows, 128]
   PagedPool pool;
@@ -298,6 +318,7 @@ __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__
     const long long prow = ((static_cast<long long>(entry.x) * p.Hkv + head) << p.page_shift) + run * 16;
     const long long drow = (static_cast<long long>(seq) * p.Hkv + head) * p.rows + j0;
     uint4* dense = p.dense[kv] + drow * 16;
+    const bool whole = (reinterpret_cast<uintptr_t>(dense) & 31u) == 0u;
     uint8_t* page = (kv ? p.pool.v : p.pool.k) + prow * (kE4m3 ? 128 : 256);
     uint8_t* scale = kE4m3 ? (kv ? p.pool.vs : p.pool.ks) + prow : nullptr;
     if (!kE4m3) {
@@ -317,10 +338,7 @@ __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__
       for (int i = 0; i < 4; ++i) {
         const int row = 4 * i + sub;
         x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-        if (row < live) {
-          x[i][0] = dense[row * 16 + 2 * e];
-          x[i][1] = dense[row * 16 + 2 * e + 1];
-        }
+        if (row < live) load32(dense + row * 16 + 2 * e, x[i][0], x[i][1], whole);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -354,8 +372,7 @@ __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__
         const int row = 4 * i + sub;
         if (row < live) {
           const float s = e8m0_value(sc[i]);
-          dense[row * 16 + 2 * e] = dequant8(make_uint2(x[i].x, x[i].y), s);
-          dense[row * 16 + 2 * e + 1] = dequant8(make_uint2(x[i].z, x[i].w), s);
+          store32(dense + row * 16 + 2 * e, dequant8(make_uint2(x[i].x, x[i].y), s), dequant8(make_uint2(x[i].z, x[i].w), s), whole);
         }
       }
     }
