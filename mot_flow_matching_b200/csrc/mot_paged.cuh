@@ -118,12 +118,16 @@ int log2_of(int v) {
 // multiple of `granule` keys, and its ranges are merged on the device. The
 // cheaper by this count of work, in granules: a unit's prologue and epilogue cost
 // `unit`, a range of a split tile `split` more (its partial result and the
-// merge). Measured: few rows, 128 keys of a warp group against a merge of about
-// 2 us; 256 rows, 2 us a key tile, 3 us a unit, 4-5 us more a range.
+// merge), and a share is at least `min_share`, one more where tiles have more than
+// 24 granules (a single sequence would be cut into too many ranges). Measured. Few
+// rows: 400 keys of one sequence 6.5 us in ranges of 128 keys against 8.0 in 256,
+// 4496 keys 9.8 against 9.4; 64 sequences of 1000 keys 32 us (e4m3) with these
+// costs, 37.5 with a unit at 1 and a split at 0. 256 rows: 2 us a key tile, 3 us
+// a unit, 4-5 us more a range.
 struct CutRule {
   int granule, unit, split, min_share;
 };
-constexpr CutRule kCutRules[2] = {{128, 1, 0, 3}, {kTileKeys, 2, 2, 5}};
+constexpr CutRule kCutRules[2] = {{128, 2, 2, 5}, {kTileKeys, 2, 2, 5}};
 
 struct PagedTile {
   int seq, row0, keys;
@@ -187,9 +191,13 @@ bool cut_units(const std::vector<PagedTile>& tiles, int heads, int ctas, long lo
 bool plan_units(const std::vector<PagedTile>& tiles, int heads, int ctas, const CutRule& rule, PagedUnit* units,
                 int unit_cap, int* cta_unit0, int* n_units) {
   long long total = 0;
-  for (const PagedTile& tl : tiles) total += static_cast<long long>(granules_of(tl, rule) + rule.unit) * heads;
+  int longest = 0;
+  for (const PagedTile& tl : tiles) {
+    total += static_cast<long long>(granules_of(tl, rule) + rule.unit) * heads;
+    longest = std::max(longest, granules_of(tl, rule));
+  }
   // smallest share that fits
-  long long lo = std::max<long long>(rule.min_share, (total + ctas - 1) / ctas), hi = lo;
+  long long lo = std::max<long long>(rule.min_share + (longest > 24), (total + ctas - 1) / ctas), hi = lo;
   while (!cut_units(tiles, heads, ctas, hi, rule, nullptr, 0, nullptr, nullptr)) {
     lo = hi + 1;
     hi *= 2;
