@@ -36,9 +36,17 @@ struct PagedTables {
 
 static_assert(TileSmem::bytes(true) <= 232448, "shared memory");
 
-// Query rows (tokens times heads of the group) up to which a sequence goes to
-// the few-rows kernel.
-constexpr int kSmallMaxRows = 2 * kSmallRows;
+// Query rows (tokens times heads of the group) up to which a sequence goes to the
+// few-rows kernel, which reads the keys once for every 8 of them; `mid`: how many
+// (sequence, KV head) pairs have 9 to 32 rows. A rule on q_len alone, so that a
+// captured call keeps its launches. Measured, us of the few-rows | the 256-row
+// kernel at 16 / 24 / 32 rows: bf16, 1 sequence of 4000 keys 12.5 / 14 / 15 | 24,
+// 8 of 2000 24 / 31 / 34 | 24, 64 of 2000 165 / 204 / 312 | 105; e4m3 11.6 / 12.8 /
+// 13.5 | 28, 20.5 / 27 / 30 | 32, 105 / 153 / 196 | 157.
+constexpr int kSmallMaxRows = 32;
+int small_rows(bool e4m3, long long mid) {
+  return e4m3 ? (mid <= 64 ? 32 : 24) : mid <= 16 ? 24 : mid <= 64 ? 16 : 8;
+}
 
 PagedTables paged_tables(const mot_paged_config& c, const int (&ctas)[2]) {
   PagedTables t;
@@ -438,6 +446,10 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
     int q0 = 0, e0 = 0;
     bool repeated = false;
     const int group = c.n_q_heads / c.n_kv_heads;
+    long long mid = 0;
+    for (int b = 0; b < batch; ++b)
+      if (q_len[b] * group > kSmallRows && q_len[b] * group <= kSmallMaxRows) mid += c.n_kv_heads;
+    const int few = small_rows(c.kv_dtype == MOT_PAGED_E4M3, mid);
     for (int b = 0; b < batch; ++b) {
       const int used = (kv_len[b] + c.page_size - 1) >> shift, past = kv_len[b] - q_len[b];
       const int* row = table + static_cast<size_t>(b) * table_stride;
@@ -464,7 +476,7 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
         w[t.tok + 2 * (q0 + i)] = pos;
         w[t.tok + 2 * (q0 + i) + 1] = row[pos >> shift];
       }
-      const int rows = q_len[b] * group, kind = rows <= kSmallMaxRows ? 0 : 1, step = kind ? kTileRows : kSmallRows;
+      const int rows = q_len[b] * group, kind = rows <= few ? 0 : 1, step = kind ? kTileRows : kSmallRows;
       for (int r = 0; r < rows; r += step) {
         const int last = std::min(rows, r + step) - 1;
         tiles[kind].push_back(PagedTile{b, r, std::max(vis, past + last / group + 1)});
