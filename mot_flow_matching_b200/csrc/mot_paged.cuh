@@ -135,7 +135,7 @@ int log2_of(int v) {
 struct CutRule {
   int granule, unit, split, min_share;
 };
-constexpr CutRule kCutRules[2] = {{128, 2, 2, 5}, {kTileKeys, 2, 2, 5}};
+constexpr CutRule kCutRules[2] = {{128, 2, 2, 5}, {kTileKeys, 2, 2, 7}};
 
 struct PagedTile {
   int seq, row0, keys;
