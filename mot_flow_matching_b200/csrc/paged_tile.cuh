@@ -21,7 +21,8 @@
 // tile's largest scale goes into the scores (keys), and into the weights
 // relative to the largest so far (values), as one factor per tile; queries are
 // made f16 in place, each row scaled by a power of two that its thread puts back. The registers are split
-// by setmaxnreg: 2 x 192 + 2 x 64 of the 4 x 128 a thread the block starts with.
+// by setmaxnreg: 2 x 192 + 2 x 64 (e4m3: 176 and 80) of the 4 x 128 a thread that
+// the block starts with.
 //
 // Probabilities are of the values' type, since they meet them in one MMA: bf16
 // ones lose about what the bf16 output itself does (half a step, averaged over
@@ -90,23 +91,27 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
   return static_cast<uint32_t>((piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// Sixteen e4m3 times 2^(b - ref) as f16 (b <= ref, or b = 255: NaN).
-__device__ __forceinline__ void e4m3x16_f16(const uint4& x, uint32_t b, uint32_t ref, uint4& lo, uint4& hi) {
+// f16 pair of 2^(b - ref) (b <= ref, or b = 255: NaN); where no b of the tile is
+// 255 or more than 14 below ref, b * 0x04000400 + near_base(ref) is the same.
+__device__ __forceinline__ uint32_t near_base(uint32_t ref) { return 0x3c003c00u - ref * 0x04000400u; }
+__device__ __forceinline__ uint32_t far_factor(uint32_t b, uint32_t ref) {
   const int d = static_cast<int>(ref) - static_cast<int>(b);
-  uint32_t f = d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
-  if (b == 255u) f = 0x7e00u;
-  f |= f << 16;
+  const uint32_t f = b == 255u ? 0x7e00u : d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  return f | (f << 16);
+}
+
+// eight e4m3 times a factor (a pair of it) as f16
+__device__ __forceinline__ uint4 e4m3x8_f16(uint2 w, uint32_t f) {
   const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
-  uint32_t r[8];
+  uint32_t r[4];
+  e4m3x4_f16x4(w.x, r[0], r[1]);
+  e4m3x4_f16x4(w.y, r[2], r[3]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e4m3x4_f16x4(word(x, i), r[2 * i], r[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&r[i]), f2);
     r[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  lo = make_uint4(r[0], r[1], r[2], r[3]);
-  hi = make_uint4(r[4], r[5], r[6], r[7]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // max of a row's 128 scores, in four chains; NaN comes out as NaN
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   const int u_begin = p.cta_unit0[blockIdx.x], u_end = p.cta_unit0[blockIdx.x + 1];
 
   if (warp >= 8 && warp < 12) {
-    regs_down<64>();
+    regs_down<kE4m3 ? 80 : 64>();
     if constexpr (kE4m3) {
       // ---------------------------------------------------------- e4m3 pages, bf16 queries -> f16 operand tiles
       // eight lanes a row, four rows a warp at a time
@@ -290,34 +295,57 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             const uint8_t* scale = smem + TileSmem::kScale + kv * 128;
             uint8_t* dst = (kv ? sV : sK) + s * T32;
             // the tile's largest scale: lane i looks at rows 4i..4i+3; NaN rows and those behind the last key do not count
-            uint32_t top = 0u;
+            uint32_t top = 0u, low = 255u;
             {
               const uint32_t w = reinterpret_cast<const uint32_t*>(scale)[lane];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint32_t b = (w >> (8 * i)) & 255u;
-                if (4 * lane + i < live && b != 255u) top = max(top, b);
+                if (4 * lane + i < live) {
+                  if (b != 255u) top = max(top, b);
+                  low = min(low, b == 255u ? 0u : b);
+                }
               }
             }
             const uint32_t ref = __reduce_max_sync(0xffffffffu, top);
+            const bool near = live == kTileKeys && ref - __reduce_min_sync(0xffffffffu, low) <= 14u;
+            // Pieces 2e and 2e + 1 of a row; lanes of the second 64 dims take the odd one first, so that the eight
+            // lanes of a row hit all banks once. All of a tile is read before its place in the ring is waited for.
+            uint2 x0[8], x1[8];
+            uint32_t f[8];
+            {
+              const uint8_t* src = raw + sub * 128 + e * 16;
+              const uint32_t base = near_base(ref);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                x0[i] = *reinterpret_cast<const uint2*>(src + (odd ? 8 : 0) + i * 2048);
+                x1[i] = *reinterpret_cast<const uint2*>(src + (odd ? 0 : 8) + i * 2048);
+                f[i] = scale[16 * i + sub];
+              }
+              if (near) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = f[i] * 0x04000400u + base;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  f[i] = far_factor(f[i], ref);
+                  // what lies behind the last key must not reach the sum, whatever it is
+                  if (16 * i + sub >= live) {
+                    f[i] = 0u;
+                    x0[i] = x1[i] = make_uint2(0u, 0u);
+                  }
+                }
+              }
+            }
             mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((it >> 1) & 1) ^ 1u, wg);
             if (ct == 0) refs[kv * 4 + (it & 3)] = ref;
-            auto put = [&](int r, const uint4& lo, const uint4& hi) {
-              // lanes of the second box store their odd piece first: the eight lanes of a row then hit all banks once
-              *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 1 : 0))) = odd ? hi : lo;
-              *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * e + (odd ? 0 : 1))) = odd ? lo : hi;
-            };
-#pragma unroll 4
+            uint8_t* dst0 = dst + tile_offset(sub, 2 * e + (odd ? 1 : 0));
+            uint8_t* dst1 = dst + tile_offset(sub, 2 * e + (odd ? 0 : 1));
+#pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int r = 16 * i + sub;
-              uint4 lo, hi;
-              e4m3x16_f16(*reinterpret_cast<const uint4*>(raw + r * 128 + e * 16), scale[r], ref, lo, hi);
-              put(r, lo, hi);
+              *reinterpret_cast<uint4*>(dst0 + i * 2048) = e4m3x8_f16(x0[i], f[i]);
+              *reinterpret_cast<uint4*>(dst1 + i * 2048) = e4m3x8_f16(x1[i], f[i]);
             }
-            // what lies behind the last key must not reach the sum, whatever it is
-            if (live < kTileKeys)
-              for (int r = sub; r < kTileKeys; r += 16)
-                if (r >= live) put(r, make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -361,7 +389,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       }
     }
   } else if (warp >= 12) {
-    regs_down<64>();
+    regs_down<kE4m3 ? 80 : 64>();
     if (warp == 13) {
       // ---------------------------------------------------------- query tiles, a unit ahead
       int n_unit[2] = {0, 0};
@@ -538,7 +566,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     }
   } else {
     // ------------------------------------------------------------ softmax, one thread per query row
-    regs_up<192>();
+    regs_up<kE4m3 ? 176 : 192>();
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
