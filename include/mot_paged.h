@@ -41,8 +41,12 @@
  *   - append, store, load and attend may be captured into a CUDA graph; a
  *     captured call may be replayed after mot_paged_batch_set has given the
  *     batch other kv_len, visible or tables, as long as batch and q_len are
- *     those of the capture. mot_paged_batch_set itself is refused on a
- *     capturing stream.
+ *     those of the capture and n_pages and the longest kv_len are within the
+ *     captured pool's pages and dense rows. mot_paged_batch_set itself is
+ *     refused on a capturing stream.
+ *   - Outputs must not overlap inputs.
+ *   - After MOT_ERR_TIMEOUT from mot_paged_get_device_status set the batch again
+ *     before it is used.
  */
 #ifndef MOT_PAGED_H
 #define MOT_PAGED_H

@@ -545,7 +545,7 @@ mot_status mot_paged_append(mot_paged_t h, mot_paged_batch_t bt, const void* qkv
   if (cs != MOT_OK) return cs;
   if (bt->repeated_written) return MOT_ERR_INVALID_ARGUMENT;
   if (bt->tokens == 0) return MOT_OK;
-  if (!qkv || !q) return MOT_ERR_INVALID_ARGUMENT;
+  if (!qkv || !q || qkv == q) return MOT_ERR_INVALID_ARGUMENT;
   if (!aligned16(qkv) || !aligned16(q)) return MOT_ERR_ALIGNMENT;
   const mot_paged_config& c = h->cfg;
   PagedAppendParams p{};
@@ -596,7 +596,7 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
   const mot_status cs = check_paged_call(h, bt, pool);
   if (cs != MOT_OK) return cs;
   if (bt->tokens == 0) return MOT_OK;
-  if (!q || !o || !workspace) return MOT_ERR_INVALID_ARGUMENT;
+  if (!q || !o || q == o || !workspace) return MOT_ERR_INVALID_ARGUMENT;
   const void* ptrs[] = {q, o, lse, workspace};
   for (const void* ptr : ptrs)
     if (ptr && !aligned16(ptr)) return MOT_ERR_ALIGNMENT;

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__
     const int head = static_cast<int>(r % p.Hkv);
     const int4 entry = p.entries[r / p.Hkv];
     const int seq = entry.y, j0 = entry.z + run * 16;
-    const int live = entry.w - run * 16;  // rows of this run that the sequence has
+    const int live = min(entry.w, p.rows - entry.z) - run * 16;  // rows of this run that the sequence (and the dense cache) has
     if (!waited) {
       grid_dep_wait();
       waited = true;

@@ -254,6 +254,75 @@ def test_attend_is_deterministic_and_leaves_its_inputs(cuda_ready):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows_per_seq", [1, 2, 3, 4, 6, 7, 8, 9])
+def test_attend_around_the_choice_of_kernel(cuda_ready, rows_per_seq, kv):
+    # 4 heads a group: 4 to 36 query rows, few and many sequences
+    run_attend(8, 2, 32, kv, [rows_per_seq], [300], seed=rows_per_seq)
+    kv_len = [rows_per_seq + 37 * i for i in range(40)]
+    run_attend(8, 2, 32, kv, [rows_per_seq] * 40, kv_len, seed=rows_per_seq, sample=2)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attend_scales_far_apart(cuda_ready, kv):
+    # rows whose magnitudes span 2^-40 .. 2^20 within a tile (8-bit scales far from the tile's largest)
+    q_len, kv_len = [1, 60], [200, 300]
+    paged, _ = make_paged(4, 2, 16, kv, q_len, kv_len)
+    table, n_pages = make_table(kv_len, 16, 3)
+    pool = fill_pool(paged, n_pages, 0)
+    g = np.random.default_rng(1)
+    dense = []
+    for what in range(2):
+        e = g.integers(-40, -3, size=(2, 2, 300, 1)) if what == 0 else g.integers(-40, 20, size=(2, 2, 300, 1))
+        dense.append(torch.from_numpy(g.normal(size=(2, 2, 300, 128)) * np.exp2(e)).to(torch.bfloat16).cuda())
+    batch = paged.new_batch()
+    batch.set(q_len, kv_len, table, n_pages)
+    paged.store(batch, *dense, pool)
+    q = torch.randn(61, 4, 128).to(torch.bfloat16).cuda()
+    lse = torch.empty(61, 4, device="cuda")
+    o = paged.attend(batch, q, pool, lse=lse)
+    check_attend(paged, pool, table, q, q_len, kv_len, [0, 0], o, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attend_query_rows_that_are_not_finite_stay_alone(cuda_ready, kv):
+    paged, pool, table, batch, q, o, lse = run_attend(4, 2, 32, kv, [1, 70], [100, 300], seed=21)
+    q2 = q.clone()
+    q2[0, 1, 3] = float("nan")
+    q2[40, 2, 7] = float("inf")
+    o2 = paged.attend(batch, q2, pool)
+    bad = torch.zeros(71, 4, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[40, 2] = True
+    assert torch.isnan(o2[bad]).all()
+    assert torch.equal(o2[~bad].view(torch.int16), o[~bad].view(torch.int16))
+
+
+def test_attend_and_load_into_16_byte_aligned_outputs(cuda_ready):
+    # outputs that start in the middle of a 32-byte sector
+    for kv in ("bf16", "e4m3"):
+        paged, pool, table, batch, q, o, _ = run_attend(8, 2, 64, kv, [1, 100, 9], [70, 300, 600], seed=9, sample=3)
+        buf = torch.zeros(o.numel() + 16, dtype=torch.bfloat16, device="cuda")
+        o2 = buf[8:8 + o.numel()].view(o.shape)
+        assert o2.data_ptr() % 32 == 16
+        paged.attend(batch, q, pool, o=o2)
+        assert torch.equal(o2.view(torch.int16), o.view(torch.int16)) and (buf[:8] == 0).all() and (buf[-8:] == 0).all()
+        k, v = paged.load(batch, pool)
+        kb = torch.zeros(k.numel() + 16, dtype=torch.bfloat16, device="cuda")
+        k2 = kb[8:8 + k.numel()].view(k.shape)
+        k2.copy_(k)
+        paged.load(batch, pool, k=k2, v=v.clone())
+        assert torch.equal(k2.view(torch.int16), k.view(torch.int16)) and (kb[:8] == 0).all() and (kb[-8:] == 0).all()
+        p2 = paged.new_pool(pool.k.shape[0])
+        for a, b in ((p2.k, pool.k), (p2.v, pool.v), (p2.k_scale, pool.k_scale), (p2.v_scale, pool.v_scale)):
+            if a is not None:
+                a.view(torch.uint8).copy_(b.view(torch.uint8))
+        b0 = paged.new_batch()
+        b0.set([0, 0, 0], [70, 300, 600], table, pool.k.shape[0])
+        paged.store(b0, k2, v, p2)
+        ka, va = paged.load(b0, p2)
+        assert torch.equal(ka[2].view(torch.int16), k[2].view(torch.int16))
+
+
 # ------------------------------------------------------------------ append
 def check_append(paged, w, pool, before, table, qkv, q_len, kv_len, q):
     c = paged.cfg
@@ -308,6 +377,9 @@ def check_append(paged, w, pool, before, table, qkv, q_len, kv_len, q):
     (16, 1, 128, [130, 129], [130, 500]),
     (32, 8, 64, [400, 231], [400, 631]),
     (5, 1, 16, [3], [3]),
+    (32, 8, 64, [1000, 0, 701], [1100, 3, 701]),  # a warp a token
+    (6, 2, 32, [3000, 1900], [3000, 2000]),
+    (7, 7, 16, [700], [701]),
 ])
 def test_append(cuda_ready, hq, hkv, page, q_len, kv_len, kv):
     paged, w = make_paged(hq, hkv, page, kv, q_len, kv_len)
@@ -532,6 +604,38 @@ def test_stream_order_without_synchronisation(cuda_ready):
             assert torch.equal(a[i, :, :n].view(torch.int16), b[i, :, :n].view(torch.int16))
 
 
+def test_batches_set_in_turn_without_synchronisation(cuda_ready):
+    # one batch object described anew before every call, different lengths, kinds of kernels and pages each time, and
+    # two batches on one workspace: as each by itself
+    paged, _ = make_paged(8, 2, 16, "bf16", [64, 64, 64], [500, 500, 500], max_batch=3)
+    table, n_pages = make_table([500, 500, 500], 16, 1)
+    pool = fill_pool(paged, n_pages, 0)
+    write_sequences(paged, pool, table, [500, 500, 500], 3)
+    cases = [([1, 1, 1], [500, 20, 3]), ([64, 1, 30], [64, 499, 77]), ([3, 0, 0], [3, 0, 0]), ([5, 64, 0], [400, 500, 9]),
+             ([1, 2, 1], [17, 300, 450])]
+    qs = [torch.randn(sum(q), 8, 128).to(torch.bfloat16).cuda() for q, _ in cases]
+    alone = []
+    for (q_len, kv_len), q in zip(cases, qs):
+        b = paged.new_batch()
+        b.set(q_len, kv_len, table, n_pages)
+        alone.append(paged.attend(b, q, pool))
+        torch.cuda.synchronize()
+    one, two = paged.new_batch(), paged.new_batch()
+    ws = one.workspace()
+    got = []
+    for turn in range(8):
+        for i, ((q_len, kv_len), q) in enumerate(zip(cases, qs)):
+            b = (one, two)[(turn + i) & 1]
+            b.set(q_len, kv_len, table, n_pages)
+            got.append((i, paged.attend(b, q, pool, workspace=ws), paged.load(b, pool)[0]))
+    torch.cuda.synchronize()
+    for i, o, k in got:
+        assert torch.equal(o.view(torch.int16), alone[i].view(torch.int16)), i
+        for s, n in enumerate(cases[i][1]):
+            ref = sequence_rows(as_f64(pool.k), table, s, n, 16)
+            assert np.array_equal(as_f64(k[s, :, :n]), ref)
+
+
 # ------------------------------------------------------------------ refusals
 def test_refusals(cuda_ready):
     paged, _ = make_paged(4, 2, 16, "bf16", [4, 4], [40, 40])
@@ -571,6 +675,8 @@ def test_refusals(cuda_ready):
         big = torch.empty(8 * 4 * 128 + 8, dtype=torch.bfloat16, device="cuda")
         paged.attend(batch, big[1:1 + 8 * 4 * 128].view(8, 4, 128), pool)
     assert e.value.status == _abi.MOT_ERR_ALIGNMENT
+    with pytest.raises(_abi.MotError):
+        paged.attend(batch, q, pool, o=q)  # over its own input
     for bad in (q[:7], q.float(), q.cpu(), q.transpose(0, 1).contiguous().transpose(0, 1)):
         with pytest.raises(ValueError):
             paged.attend(batch, bad, pool)
