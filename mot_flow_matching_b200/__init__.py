@@ -8,4 +8,4 @@ not load the library; the first call into ``layer`` does, and fails loudly if
 it is missing.
 """
 
-__all__ = ["synth", "layer", "build"]
+__all__ = ["synth", "layer", "mlp", "moe", "step", "paged", "build"]

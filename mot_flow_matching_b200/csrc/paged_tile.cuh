@@ -3,7 +3,7 @@
 //
 // A unit is 256 query rows of one (sequence, KV head) -- (token, head of the
 // group) pairs, head fastest, as two 128-row tiles -- and a range of 128-key
-// tiles. Per key tile S_t = Q_t K^T into TMEM, softmax in registers, P_t (bf16
+// tiles. Per key tile S_t = Q_t K^T into TMEM, softmax in registers, P_t (16-bit
 // pairs) over S_t's own columns, O_t += P_t V with P_t as the TMEM operand; the
 // tensor core works on one query tile while the other's softmax runs. One CTA
 // per SM runs its list of units back to back.
@@ -20,15 +20,28 @@
 // to 2^-15 of the largest; below that a value is off by at most 2^-25 of it). The
 // tile's largest scale goes into the scores (keys), and into the weights
 // relative to the largest so far (values), as one factor per tile; queries are
-// made f16 in place, each row scaled by a power of two that its thread puts back. The registers are split
-// by setmaxnreg: 2 x 192 + 2 x 64 (e4m3: 176 and 80) of the 4 x 128 a thread that
-// the block starts with.
+// made f16 in place, each row scaled by a power of two that its thread puts back.
+// The registers are split by setmaxnreg: 2 x 192 + 2 x 64 (e4m3: 176 and 80) of
+// the 4 x 128 a thread that the block starts with.
 //
 // Probabilities are of the values' type, since they meet them in one MMA: bf16
 // ones lose about what the bf16 output itself does (half a step, averaged over
 // the keys), f16 ones an eighth of that; the row sum is taken in f32 from the
-// unrounded ones. The running max is raised, and O_t
-// rescaled through TMEM, only when a row's max grows by more than 2^8.
+// unrounded ones. The running max is raised, and O_t rescaled through TMEM, only
+// when a row's max grows by more than 2^8.
+//
+// What bounds it, measured on one B200: per key tile and pair of query tiles the
+// MMAs take 2048 clocks (64 each, on one SM as on all), while by time stamps in
+// the kernel a query tile's chain S -> softmax -> P V -> next S takes about 3000:
+// 950 waiting for S, 170 to read it, 200 for the max, 1500 for exponentials and P
+// (1024 of the MUFU). Two query tiles overlap but do not hide it, and TMEM has no
+// room for a third. 2 x 4096 image tokens over 4496 keys (603 GFLOP): 547 us back
+// to back (1.10 PFLOP/s), the first launches after a pause 475 us (1.27). Prompt
+// chunks of 129 to 512 tokens, bf16: 74 us. Tried against the kernel of the time
+// and slower: a quarter of the exponentials by polynomial (image 564 against 555
+// us, a mixed e4m3 batch 289 against 269), a second MMA warp (image 565 against
+// 552), e4m3 conversion on eight warps with fewer registers for the softmax (the
+// mixed batch 272 against 251; 233 now).
 #pragma once
 
 #include "paged.cuh"
