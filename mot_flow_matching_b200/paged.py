@@ -36,10 +36,16 @@ def mot_paged_create(cfg: MotPagedConfig, weights: Dict[str, torch.Tensor], stre
 def _host_i32(v, name: str) -> Optional[torch.Tensor]:
     if v is None:
         return None
-    t = torch.as_tensor(v, dtype=torch.int32)
+    t = torch.as_tensor(v)
     if t.is_cuda:
         raise ValueError(f"{name} must be host memory (got {t.device})")
-    return t.contiguous()
+    if t.dtype != torch.int32 and t.numel():
+        if t.is_floating_point() or t.is_complex():
+            raise ValueError(f"{name} must be integers (got {t.dtype})")
+        t = t.to(torch.int64)
+        if int(t.min()) < -2 ** 31 or int(t.max()) >= 2 ** 31:
+            raise ValueError(f"{name} must fit in 32 bits (got {int(t.min())} to {int(t.max())})")
+    return t.to(torch.int32).contiguous()
 
 
 def mot_paged_batch_set(bt, q_len, kv_len, table, n_pages: int, visible=None, stream=None) -> None:
@@ -96,6 +102,8 @@ class MotPagedBatch:
     def set(self, q_len: Sequence[int], kv_len: Sequence[int], table, n_pages: int,
             visible: Optional[Sequence[int]] = None, stream=None) -> None:
         self.batch = 0
+        if self.paged.handle is None or not self.handle:
+            raise ValueError("the batch or its handle has been closed")
         mot_paged_batch_set(self.handle, q_len, kv_len, table, n_pages, visible, stream)
         self.batch, self.tokens, self.kv_max = len(q_len), int(sum(q_len)), int(max(kv_len))
         c = self.paged.cfg

@@ -117,6 +117,30 @@ def test_bindings_refuse_host_tensors():
         MotPagedPool(pages[..., :64], pages[..., :64])
 
 
+def test_bindings_refuse_lengths_and_pages_that_are_not_32_bit_integers():
+    from mot_flow_matching_b200.paged import mot_paged_batch_set
+    good = dict(q_len=[1, 1], kv_len=[3, 4], table=[[0], [1]], visible=[0, 0])
+    for name in good:
+        for bad in (torch.tensor(good[name]).double(), torch.tensor(good[name]) + 2 ** 32,
+                    torch.tensor(good[name]) - 2 ** 32):
+            with pytest.raises(ValueError, match=name):
+                mot_paged_batch_set(None, n_pages=2, **{**good, name: bad})
+    with pytest.raises(ValueError, match="q_len must be integers"):
+        mot_paged_batch_set(None, n_pages=2, **{**good, "q_len": [1.5, 1]})
+
+
+def test_a_closed_handle_sets_no_batch():
+    # the batch object's memory in the library refers to the handle's
+    from mot_flow_matching_b200.paged import MotPaged, MotPagedBatch
+    paged, batch = object.__new__(MotPaged), object.__new__(MotPagedBatch)
+    paged.handle, batch.paged, batch.handle = None, paged, c_void_p(16)
+    try:
+        with pytest.raises(ValueError, match="closed"):
+            batch.set([1], [1], [[0]], 1)
+    finally:
+        batch.handle = c_void_p()  # not the library's: nothing to free
+
+
 def plan(L, kind, tiles, heads, ctas, cap=None):
     t = arr(tiles).reshape(-1, 3)
     cap = len(t) * heads + ctas if cap is None else cap
