@@ -565,10 +565,10 @@ struct Unseen {
 // The batch's tables are written by copies, never by a kernel, so they are read
 // before the grid this one depends on has completed.
 // Measured, one B200: 64 single tokens over ragged e4m3 caches of 0.4 to 8.6
-// thousand keys (554 MB) 109 us, 5.1 TB/s. Under ncu the kernel takes 112 us, its loads
-// without the arithmetic 96; a plain read of as many bytes takes 78 us. A single token over 4496 bf16 keys
-// 9.6 us, of which the keys' bytes are 2.8: the rest is launch, dependent
-// loads, and the merge of 18 ranges.
+// thousand keys (554 MB) 109 us, 5.1 TB/s. Under ncu the kernel takes 112 us, its
+// loads without the arithmetic 96; a plain read of as many bytes takes 78 us. A
+// single token over 4496 bf16 keys 9.6 us, of which the keys' bytes are 2.8: the
+// rest is launch, dependent loads, and the merge of 18 ranges.
 template <bool kE4m3>
 __global__ void __launch_bounds__(SmallShape<kE4m3>::kThreads, 2)
 paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
