@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               }
             }
             const uint32_t ref = __reduce_max_sync(0xffffffffu, top);
-            const bool near = live == kTileKeys && ref - __reduce_min_sync(0xffffffffu, low) <= 14u;
+            const uint32_t least = __reduce_min_sync(0xffffffffu, low);  // 0 also where a row is NaN
+            const bool near = live == kTileKeys && least != 0u && ref - least <= 14u;
             // Pieces 2e and 2e + 1 of a row; lanes of the second 64 dims take the odd one first, so that the eight
             // lanes of a row hit all banks once. All of a tile is read before its place in the ring is waited for.
             uint2 x0[8], x1[8];

@@ -243,6 +243,25 @@ def test_attend_unseen_values_have_no_influence(cuda_ready, what, where, kv, pas
         assert not torch.isfinite(hit).any()
 
 
+@pytest.mark.parametrize("q_len", [256, 2])
+def test_attend_tile_of_nan_scales(cuda_ready, q_len):
+    # keys 128.. all have the NaN scale, over payloads that are finite (a pool need not come from append or store):
+    # queries that see one of them get NaN, the others what the oracle says
+    paged, pool, table, batch, q, _, _ = run_attend(4, 2, 16, "e4m3", [q_len], [256], seed=4, sample=4)
+    for i in table[0][8:16]:
+        pool.k_scale.view(torch.uint8)[int(i)] = 255
+        pool.v_scale.view(torch.uint8)[int(i)] = 255
+    lse = torch.empty(q_len, 4, device="cuda")
+    o = paged.attend(batch, q, pool, lse=lse)
+    free = max(0, q_len - 128)
+    assert torch.isnan(o[free:]).all() and torch.isnan(lse[free:]).all()
+    if free:
+        k, v = (sequence_rows(x, table, 0, 128, 16) for x in pool_values(pool))
+        ref, l, absv, mag = PG.chunk_attention(as_f64(q[:free]), k, v, 0)
+        assert np.all(np.abs(as_f64(o[:free]) - ref) <= attend_tolerance(ref, absv, mag, small_weights("e4m3", v)))
+        assert np.all(np.abs(as_f64(lse[:free]) - l) <= lse_tolerance(l, mag))
+
+
 def test_attend_is_deterministic_and_leaves_its_inputs(cuda_ready):
     paged, pool, table, batch, q, o, lse = run_attend(32, 8, 64, "bf16", [1, 200, 1], [3000, 900, 17], sample=2)
     k0, v0, q0 = pool.k.clone(), pool.v.clone(), q.clone()
