@@ -41,10 +41,11 @@
  *   - append, store, load and attend may be captured into a CUDA graph; a
  *     captured call may be replayed after mot_paged_batch_set has given the
  *     batch other kv_len, visible or tables, as long as batch and q_len are
- *     those of the capture and n_pages and the longest kv_len are within the
- *     captured pool's pages and dense rows. mot_paged_batch_set itself is
- *     refused on a capturing stream.
- *   - Outputs must not overlap inputs.
+ *     those of the capture, n_pages and the longest kv_len are within the
+ *     captured pool's pages and dense rows, and no page appears twice that the
+ *     captured call refuses to find twice (nothing checks a replay).
+ *     mot_paged_batch_set itself is refused on a capturing stream.
+ *   - Outputs must not overlap inputs or one another.
  *   - After MOT_ERR_TIMEOUT from mot_paged_get_device_status set the batch again
  *     before it is used.
  */
@@ -115,7 +116,7 @@ mot_status mot_paged_batch_create(mot_paged_t h, mot_paged_batch_t* out);
  * A page may appear more than once in the table (sequences that share a
  * prompt); mot_paged_append refuses a batch in which a page that a chunk is
  * written to appears twice, mot_paged_store one in which any page does.
- * Enqueues one copy on `stream`. */
+ * Enqueues its copies on `stream`. */
 mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_t* q_len, const int32_t* kv_len,
                                const int32_t* visible, const int32_t* table, int32_t table_stride, int32_t n_pages,
                                void* stream);
@@ -160,8 +161,8 @@ mot_status mot_paged_load(mot_paged_t h, mot_paged_batch_t bt, const mot_paged_p
  *   workspace  device, workspace_bytes from mot_paged_query_workspace
  * Rows of a page behind kv_len are never used, whatever they hold. An infinity
  * or NaN among the cached rows reaches the outputs of the queries that see it
- * (as NaN or infinity), and of no others. Scores, statistics and sums are f32; a result does not
- * depend on timing (fixed order of every sum). */
+ * (as NaN or infinity), and of no others. Scores, statistics and sums are f32;
+ * a result does not depend on timing (fixed order of every sum). */
 mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, const mot_paged_pool* pool, void* o,
                             float* lse, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -280,8 +280,8 @@ bool map_bytes(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows
 mot_status paged_copy(mot_paged_t h, mot_paged_batch_t bt, void* k, void* v, int32_t rows, const mot_paged_pool* pool,
                       bool store, cudaStream_t st) {
   if (rows < bt->kv_max || (store && bt->repeated)) return MOT_ERR_INVALID_ARGUMENT;
-  if (bt->entries == 0) return MOT_OK;
-  if (!k || !v) return MOT_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MOT_OK;
+  if (!k || !v || (!store && k == v)) return MOT_ERR_INVALID_ARGUMENT;
   if (!aligned16(k) || !aligned16(v)) return MOT_ERR_ALIGNMENT;
   const mot_paged_config& c = h->cfg;
   PagedCopyParams p{};
@@ -294,7 +294,8 @@ mot_status paged_copy(mot_paged_t h, mot_paged_batch_t bt, void* k, void* v, int
   p.Hkv = c.n_kv_heads;
   p.page_shift = log2_of(c.page_size);
   const long long items = static_cast<long long>(bt->entries) * c.n_kv_heads * 2 * (c.page_size / 16);
-  const int grid = static_cast<int>(std::min<long long>((items + 7) / 8, 128ll * h->num_sms));
+  // launched for an empty batch too: a captured call must find what the batch holds when it is replayed
+  const int grid = static_cast<int>(std::min<long long>(std::max<long long>((items + 7) / 8, 1), 128ll * h->num_sms));
   const bool e4m3 = c.kv_dtype == MOT_PAGED_E4M3;
   auto kern = e4m3 ? (store ? paged_copy_kernel<true, true> : paged_copy_kernel<true, false>)
                    : (store ? paged_copy_kernel<false, true> : paged_copy_kernel<false, false>);

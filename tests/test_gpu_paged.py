@@ -588,6 +588,47 @@ def test_append_then_attend_in_a_graph_follows_the_batch(cuda_ready):
             assert torch.equal(o.view(torch.int16), eager[i][1].view(torch.int16))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_copies_captured_empty_follow_the_batch(cuda_ready, kv):
+    # store and load captured while every sequence is empty, replayed over sequences that are not
+    paged, _ = make_paged(4, 2, 16, kv, [0, 0], [40, 7])
+    table, n_pages = make_table([40, 7], 16, 2)
+    pool = fill_pool(paged, n_pages, 0)
+    k, v = (torch.randn(2, 2, 40, 128).to(torch.bfloat16).cuda() for _ in range(2))
+    k2, v2 = torch.full_like(k, -3.0), torch.full_like(v, -3.0)
+    batch, side = paged.new_batch(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        batch.set([0, 0], [0, 0], table, n_pages)
+        graph = torch.cuda.CUDAGraph()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            paged.store(batch, k, v, pool)
+            paged.load(batch, pool, k2, v2)
+        graph.replay()
+        side.synchronize()
+        assert (k2 == -3).all() and (v2 == -3).all()
+        batch.set([0, 0], [40, 7], table, n_pages)
+        graph.replay()
+        side.synchronize()
+    for x, y, what in ((k, k2, 0), (v, v2, 1)):
+        for b, n in enumerate((40, 7)):
+            assert np.array_equal(as_f64(y[b, :, :n]), sequence_rows(pool_values(pool)[what], table, b, n, 16))
+            if kv == "bf16":
+                assert torch.equal(x[b, :, :n].view(torch.int16), y[b, :, :n].view(torch.int16))
+        assert (y[1, :, 7:] == -3).all()
+
+
+def test_load_refuses_one_tensor_for_both(cuda_ready):
+    paged, _ = make_paged(4, 2, 16, "bf16", [1], [20])
+    batch, pool = paged.new_batch(), paged.new_pool(2)
+    batch.set([1], [20], [[0, 1]], 2)
+    k = torch.empty(1, 2, 20, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(_abi.MotError) as e:
+        paged.load(batch, pool, k, k)
+    assert e.value.status == _abi.MOT_ERR_INVALID_ARGUMENT
+
+
 def test_stream_order_without_synchronisation(cuda_ready):
     # set, append, attend, load issued back to back on a stream of its own equal the synchronised run
     hq, hkv, page, q_len, kv_len = 8, 2, 32, [40, 1], [300, 1000]
