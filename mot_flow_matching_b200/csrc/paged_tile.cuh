@@ -41,7 +41,7 @@
 // and slower: a quarter of the exponentials by polynomial (image 564 against 555
 // us, a mixed e4m3 batch 289 against 269), a second MMA warp (image 565 against
 // 552), e4m3 conversion on eight warps with fewer registers for the softmax (the
-// mixed batch 272 against 251; 233 now).
+// mixed batch 272 against 251; 240 now).
 #pragma once
 
 #include "paged.cuh"
@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               }
             }
             const uint32_t ref = __reduce_max_sync(0xffffffffu, top);
-            const uint32_t least = __reduce_min_sync(0xffffffffu, low);  // 0 also where a row is NaN
+            // 0 also where a row is NaN (other forms of this test, one or two instructions shorter, were no faster)
+            const uint32_t least = __reduce_min_sync(0xffffffffu, low);
             const bool near = live == kTileKeys && least != 0u && ref - least <= 14u;
             // Pieces 2e and 2e + 1 of a row; lanes of the second 64 dims take the odd one first, so that the eight
             // lanes of a row hit all banks once. All of a tile is read before its place in the ring is waited for.
