@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               }
             }
             const uint32_t ref = __reduce_max_sync(0xffffffffu, top);
-            // 0 also where a row is NaN (other forms of this test, one or two instructions shorter, were no faster)
+            // 0 also where a row is NaN (a signed minimum, or a larger least `ref`, took as long)
             const uint32_t least = __reduce_min_sync(0xffffffffu, low);
             const bool near = live == kTileKeys && least != 0u && ref - least <= 14u;
             // Pieces 2e and 2e + 1 of a row; lanes of the second 64 dims take the odd one first, so that the eight
