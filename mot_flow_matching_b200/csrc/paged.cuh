@@ -559,9 +559,12 @@ struct Unseen {
 // out: on sm_100 it runs as conversions and f16 products); the dims that each
 // register pair stands for are permuted so that a lane reads whole 16-byte
 // pieces, Q alike, and the rows of O^T are consecutive dims of a lane. The
-// scales are applied in f32 to the scores and to the weights (relative to the
-// largest value scale so far, so that a weight in f16 neither overflows nor
-// loses the keys that count); queries are scaled by a power of two into f16.
+// scales are applied in f32, to the scores and to the weights: what meets the
+// values in f16 is 2^(score - max + value exponent) relative to a running max of
+// its own, per query row and over the keys that the row sees. So a key loses
+// weight only against products of weight and value that count in the same row:
+// below 2^-21 of the largest one (weights go up to 2^15) it is rounded to a
+// multiple of 2^-31 of it. Queries are scaled by a power of two into f16.
 // The batch's tables are written by copies, never by a kernel, so they are read
 // before the grid this one depends on has completed.
 // Measured, one B200: 64 single tokens over ragged e4m3 caches of 0.4 to 8.6
@@ -697,7 +700,9 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    int v_ref = 0;  // largest value scale byte so far (e4m3)
+    // e4m3: O^T counts in units of 2^(r_run - kUp), r_run the running max of score - m_run + value exponent
+    float r_run[2] = {-INFINITY, -INFINITY};
+    constexpr float kUp = 7.f;
 
     // the 16 keys from `key` on; kWhole: every row sees all of them (the other case, code of its own, is rare)
     auto take = [&](int key, auto whole_c) {
@@ -706,7 +711,7 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
         const uint32_t k_addr = smem_u32(kt) + key_w * 128;
         float s[2][4] = {};  // two sums: shorter chains
         float x[4];          // base-2 scores; x[0], x[1]: key g, rows 2c, 2c + 1; x[2], x[3]: key g + 8
-        uint32_t vs[2] = {0u, 0u};
+        [[maybe_unused]] uint32_t vs[2] = {0u, 0u};
         if constexpr (!kE4m3) {
           // k-step i: rows 0-7 | 8-15 of pieces 2i, then of 2i + 1
 #pragma unroll
@@ -749,41 +754,58 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
             vs[1] = unseen.scale(vs[1], g + 8, c);
           }
         }
-        // the running max moves only when a score passes it by 2^8
+        // the running max moves only when a score passes it by 2^8; r_run alike
         const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
         bool grow = mx0 > m_run[0] + kLazyRescaleLog2 || mx1 > m_run[1] + kLazyRescaleLog2;
-        int v_max = 0;
+        float d[4];  // base-2 logs of the weights
+        [[maybe_unused]] float y[4], vx[2];  // e4m3: with the values' exponents, and those
+        auto logs = [&] {
+          const float m0 = finite_or_zero(m_run[0]), m1 = finite_or_zero(m_run[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            d[i] = x[i] - ((i & 1) ? m1 : m0);
+            if constexpr (kE4m3) y[i] = d[i] + vx[i >> 1];
+          }
+        };
         if constexpr (kE4m3) {
-          v_max = static_cast<int>(max(vs[0], vs[1]));
-          grow = grow || v_max > v_ref;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) vx[r] = vs[r] == 255u ? NAN : static_cast<float>(static_cast<int>(vs[r]) - 127);
         }
+        logs();
+        if constexpr (kE4m3)
+          grow = grow || fmaxf(y[0], y[2]) > r_run[0] + kLazyRescaleLog2 || fmaxf(y[1], y[3]) > r_run[1] + kLazyRescaleLog2;
         if (__any_sync(0xffffffffu, grow)) {
           float a[2] = {mx0, mx1}, f[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], d));
+            for (int o = 4; o < 32; o <<= 1) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
             a[i] = fmaxf(a[i], m_run[i]);
             f[i] = ex2_approx(m_run[i] - finite_or_zero(a[i]));
+            if constexpr (kE4m3) r_run[i] = m_run[i] == -INFINITY ? -INFINITY : r_run[i] - (a[i] - m_run[i]);
             m_run[i] = a[i];
             l_run[i] *= f[i];
           }
+          logs();
           if constexpr (kE4m3) {
-            v_max = max(v_ref, __reduce_max_sync(0xffffffffu, v_max));
-            const float d = ex2_approx(static_cast<float>(v_ref - v_max));
-            f[0] *= d;
-            f[1] *= d;
-            v_ref = v_max;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float b = fmaxf(y[i], y[2 + i]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+              b = fmaxf(b, r_run[i]);
+              f[i] = ex2_approx(r_run[i] - finite_or_zero(b));
+              r_run[i] = b;
+            }
           }
 #pragma unroll
           for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[t][i] *= f[i & 1];
         }
-        const float m0 = finite_or_zero(m_run[0]), m1 = finite_or_zero(m_run[1]);
         float pr[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(x[i] - ((i & 1) ? m1 : m0));
+        for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(d[i]);
         l_run[0] += pr[0] + pr[2];
         l_run[1] += pr[1] + pr[3];
         if constexpr (!kE4m3) {
@@ -808,11 +830,7 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
         } else {
           float w[4];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float f = ex2_approx(static_cast<float>(static_cast<int>(vs[r]) - v_ref));
-            w[2 * r] = pr[2 * r] * f;
-            w[2 * r + 1] = pr[2 * r + 1] * f;
-          }
+          for (int i = 0; i < 4; ++i) w[i] = ex2_approx(y[i] - (finite_or_zero(r_run[i & 1]) - kUp));
           const uint32_t b0 = transpose_8x8(pack_half2(w[0], w[1])), b1 = transpose_8x8(pack_half2(w[2], w[3]));
           // keys 2c, 2c + 1, 2c + 8, 2c + 9, dims 16g..16g + 15: eight lanes hit all banks once
           uint4 v[4];
@@ -869,7 +887,12 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], d);
     }
-    const float unscale = kE4m3 ? e8m0_value(static_cast<uint32_t>(v_ref)) : 1.f;
+    // back to units of 1, in two steps (2^135 is no f32)
+    float half[2] = {1.f, 1.f};
+    if constexpr (kE4m3) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) half[i] = ex2_approx(0.5f * (finite_or_zero(r_run[i]) - kUp));
+    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -881,8 +904,8 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
 #pragma unroll
           for (int t = 0; t < 8; t += 4)
             *reinterpret_cast<float4*>(sum_at(warp, r, 16 * g + 8 * j + t)) =
-                make_float4(o[t][2 * j + i] * unscale, o[t + 1][2 * j + i] * unscale, o[t + 2][2 * j + i] * unscale,
-                            o[t + 3][2 * j + i] * unscale);
+                make_float4(o[t][2 * j + i] * half[i] * half[i], o[t + 1][2 * j + i] * half[i] * half[i],
+                            o[t + 2][2 * j + i] * half[i] * half[i], o[t + 3][2 * j + i] * half[i] * half[i]);
         } else {
 #pragma unroll
           for (int t = 0; t < 8; ++t) *sum_at(warp, r, 16 * t + 8 * j + g) = o[t][2 * j + i];

@@ -1,0 +1,87 @@
+"""The paged attention over its whole range of magnitudes: cached rows of very
+different size, seen and unseen. Every query is held to the fp64 oracle over the
+keys that it sees, and every bound is taken from those keys alone."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mot_paged_oracle as PG
+from tests.test_gpu_paged import (as_f64, attend_tolerance, fill_pool, lse_tolerance, make_paged, make_table, pool_values,
+                                  sequence_rows, small_weights)
+
+pytestmark = pytest.mark.gpu
+
+
+def cached(hq, hkv, page, kv, q_len, kv_len, k, v, visible=None, **kw):
+    """A pool and a batch of sequences whose dense keys and values are k, v [B, Hkv, rows, 128]."""
+    paged, _ = make_paged(hq, hkv, page, kv, q_len, kv_len, **kw)
+    table, n_pages = make_table(kv_len, page, 3)
+    pool = fill_pool(paged, n_pages, 0)
+    batch = paged.new_batch()
+    batch.set(q_len, kv_len, table, n_pages, visible=visible)
+    paged.store(batch, k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), pool)
+    return paged, pool, table, batch
+
+
+def attend(paged, pool, batch, q):
+    lse = torch.full(q.shape[:2], -7.0, device="cuda")
+    o = paged.attend(batch, q, pool, lse=lse)
+    torch.cuda.synchronize()
+    assert paged.device_status() == 0
+    return as_f64(o), as_f64(lse)
+
+
+def check_rows(paged, pool, table, q, q_len, kv_len, visible, o, lse, small=small_weights, rows=None):
+    """The queries of one sequence (`rows` of them) against the oracle over what each sees."""
+    k, v = (sequence_rows(x, table, 0, kv_len, paged.cfg.page_size) for x in pool_values(pool))
+    qf = as_f64(q)
+    for i in range(q_len) if rows is None else rows:
+        limit = max(visible, kv_len - q_len + i + 1)
+        ref, l, absv, mag = PG.chunk_attention(qf[i:i + 1], k[:, :limit], v[:, :limit], limit)
+        tol = attend_tolerance(ref, absv, mag, small(pool.kv_dtype, v[:, :limit]))
+        err = np.abs(o[i:i + 1] - ref)
+        assert np.all(err <= tol), (i, limit, float(np.nanmax(err / tol)), o[i, 0, :4], ref[0, 0, :4])
+        assert np.all(np.abs(lse[i:i + 1] - l) <= lse_tolerance(l, mag)), (i, lse[i], l)
+
+
+# 4 query heads over 2 KV heads: 2 or 3 tokens are 4 or 6 query rows of a unit of 8
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("power", [10, 17, 24, 30, 60])
+@pytest.mark.parametrize("q_len,past,where", [(2, 0, 1), (3, 300, 2), (4, 61, 1)])
+def test_rows_that_a_query_does_not_see_may_be_of_any_size(cuda_ready, q_len, past, where, power, what, kv):
+    g = torch.Generator().manual_seed(q_len + power)
+    n = past + q_len
+    dense = {x: torch.randn(1, 2, n, 128, generator=g) for x in ("k", "v")}
+    dense[what][0, :, past + where] *= 2.0 ** power
+    paged, pool, table, batch = cached(4, 2, 16, kv, [q_len], [n], dense["k"], dense["v"])
+    q = torch.randn(q_len, 4, 128, generator=g).to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+    check_rows(paged, pool, table, q, q_len, n, 0, o, lse, rows=sorted({0, 1, where // 2, where - 1, where, q_len - 1}))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [20, 40, 90])
+@pytest.mark.parametrize("big_first", [False, True])
+@pytest.mark.parametrize("q_len,n", [(1, 40), (3, 700)])
+def test_a_large_value_of_small_weight_leaves_the_others(cuda_ready, q_len, n, big_first, power, kv):
+    # Half of the keys have score 22.6 and values of 1, the others score -22.6 (weights of 2^-65) and values of 2^power:
+    # all of them seen by all queries. A weight that meets 8-bit values is a multiple of 2^-31 of the largest product of
+    # weight and value (2^7 below 1, and 2^-24 of that), off by half of one, times 448 units of which the largest value
+    # has at least 224.
+    g = torch.Generator().manual_seed(n + power)
+    u = torch.randint(0, 2, (2, 1, 128), generator=g).float() * 2 - 1
+    v = torch.randn(1, 2, n, 128, generator=g)
+    far = torch.arange(n) < n // 2
+    far = far if big_first else ~far
+    k = 0.25 * u[None] * torch.where(far, -1.0, 1.0)[None, None, :, None]
+    v[:, :, far] *= 2.0 ** power
+    paged, pool, table, batch = cached(4, 2, 16, kv, [q_len], [n], k, v, visible=[n])
+    q = (8 * u.repeat_interleave(2, 0)[:, 0])[None].expand(q_len, 4, 128).contiguous().to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+
+    def small(kv_dtype, vv):
+        s = np.where(far.numpy(), -22.6, 22.6)
+        w = np.exp(s - 22.6)
+        return len(w) * 2.0 ** -31 * (w / w.sum() * np.abs(vv).max(-1)).max() if kv_dtype == "e4m3" else 0.0
+    check_rows(paged, pool, table, q, q_len, n, n, o, lse, small=small, rows=sorted({0, q_len // 2, q_len - 1}))
