@@ -16,11 +16,13 @@
 // atom) straight into the operand tiles. e4m3 pages: boxes of raw rows and their
 // scales into a staging tile each for keys and values, from which warps 8-11
 // make f16 operand tiles: e4m3 -> f16 is one exact instruction per pair, and the
-// row's scale relative to the tile's largest is a power of two <= 1 (exact down
-// to 2^-15 of the largest; below that a value is off by at most 2^-25 of it). The
+// row's scale relative to the tile's largest an exact factor, a power of two. The
 // tile's largest scale goes into the scores (keys), and into the weights
 // relative to the largest so far (values), as one factor per tile; queries are
 // made f16 in place, each row scaled by a power of two that its thread puts back.
+// Where a unit's scales lie too far apart for that (`kKeySpan`, `kValueSpan`; warp
+// 15 reads them a unit or two ahead), the operand tiles are bf16 instead, which
+// holds payload times scale, and the queries, as they are.
 // The registers are split by setmaxnreg: 2 x 192 + 2 x 64 (e4m3: 176 and 80) of
 // the 4 x 128 a thread that the block starts with.
 //
@@ -41,7 +43,7 @@
 // and slower: a quarter of the exponentials by polynomial (image 564 against 555
 // us, a mixed e4m3 batch 289 against 269), a second MMA warp (image 565 against
 // 552), e4m3 conversion on eight warps with fewer registers for the softmax (the
-// mixed batch 272 against 251; 240 now).
+// mixed batch 272 against 251; 248 now, 239 before wide units were told apart).
 #pragma once
 
 #include "paged.cuh"
@@ -69,10 +71,10 @@ struct TileSmem {
   static constexpr uint32_t kK = kQ + 2 * kTile;
   static constexpr uint32_t kV = kK + 2 * kTile;
   static constexpr uint32_t kBar = kV + 2 * kTile;
-  static constexpr uint32_t kRaw = kBar + 256;  // e4m3: [keys, values] 128 rows of 128 bytes, then 2 x 128 scales
+  static constexpr uint32_t kRaw = kBar + 512;  // e4m3: [keys, values] 128 rows of 128 bytes, then 2 x 128 scales
   static constexpr uint32_t kRawTile = 16384;
   static constexpr uint32_t kScale = kRaw + 2 * kRawTile;
-  static constexpr uint32_t kRef = kScale + 256;   // e4m3: largest scale bytes, keys [4 tiles], values [4 tiles]
+  static constexpr uint32_t kRef = kScale + 256;   // e4m3: largest scale bytes, keys [4 tiles] (| kWide), values [4 tiles]
   static constexpr uint32_t kQScale = kRef + 64;   // e4m3: [2 units][256 rows] 127 + exponent of a query row's factor
   static constexpr uint32_t bytes(bool e4m3) { return (e4m3 ? kQScale + 512 : kRaw) + 1024; }
 };
@@ -104,13 +106,45 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
   return static_cast<uint32_t>((piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// f16 pair of 2^(b - ref) (b <= ref, or b = 255: NaN); where no b of the tile is
-// 255 or more than 14 below ref, b * 0x04000400 + near_base(ref) is the same.
+// An 8-bit unit is wide when its scales differ by more than f16 operands bear: a
+// key scale by more than 2^kKeySpan (a row's factor relative to its tile's largest
+// would no longer be exact), a value scale by more than 2^kValueSpan (weights
+// relative to the unit's largest value scale would lose bits: what f16 takes from a
+// weight is at most 2^-32 of the row's largest (weights go up to 2^15), times 448
+// units of 2^kValueSpan of a row with a largest value of at least 224: 2^-24 of
+// the largest value that a query sees, a key, whatever the size of those that it
+// does not see). Wide units run on bf16 operands, which hold every row as it is.
+constexpr int kKeySpan = 14, kValueSpan = 7;
+constexpr float kWeightUp = 7.f;  // weights of f16 units are 2^kWeightUp times as large
+constexpr uint32_t kWide = 256u;
+
+// largest and smallest scale byte of `rem` rows from `src` on (16 at most); 255 (NaN) counts as neither
+struct ScaleSpan {
+  uint32_t top = 0u, low = 0x00ff00ffu;  // pairs; top: plus 1, 0 = none
+  __device__ __forceinline__ void take(const uint4& v, int rem) {
+    const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = rem - 4 * i;
+      const uint32_t w = n >= 4 ? w4[i] : n <= 0 ? 0xffffffffu : w4[i] | (0xffffffffu << (8 * n));
+      const uint32_t a = w & 0x00ff00ffu, b = (w >> 8) & 0x00ff00ffu;
+      top = __vmaxu2(top, __vmaxu2((a + 0x00010001u) & 0x00ff00ffu, (b + 0x00010001u) & 0x00ff00ffu));
+      low = __vminu2(low, __vminu2(a, b));
+    }
+  }
+  // over the warp: largest minus smallest; negative when there is none
+  __device__ __forceinline__ int span() const {
+    const uint32_t t = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    const uint32_t l = __reduce_min_sync(0xffffffffu, min(low & 0xffffu, low >> 16));
+    return static_cast<int>(t) - 1 - static_cast<int>(l);
+  }
+};
+
+// f16 pair of 2^(b - ref) (b at most kKeySpan below ref, or 255: NaN); b * 0x04000400 +
+// near_base(ref) is the same where b is not 255.
 __device__ __forceinline__ uint32_t near_base(uint32_t ref) { return 0x3c003c00u - ref * 0x04000400u; }
-__device__ __forceinline__ uint32_t far_factor(uint32_t b, uint32_t ref) {
-  const int d = static_cast<int>(ref) - static_cast<int>(b);
-  const uint32_t f = b == 255u ? 0x7e00u : d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
-  return f | (f << 16);
+__device__ __forceinline__ uint32_t near_factor(uint32_t b, uint32_t ref) {
+  return b == 255u ? 0x7e007e00u : b * 0x04000400u + near_base(ref);
 }
 
 // eight e4m3 times a factor (a pair of it) as f16
@@ -245,9 +279,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   uint64_t* raw_full = bars + 21;   // [2] keys, values (e4m3)
   uint64_t* raw_empty = bars + 23;  // [2]
   uint64_t* q_raw = bars + 25;      // [2] query tiles before their conversion (e4m3)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
+  uint64_t* wide_full = bars + 27;   // [2] units: whether the unit is wide (e4m3)
+  uint64_t* wide_empty = bars + 29;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* last_flag = tmem_slot + 2;
+  volatile uint32_t* wide_flag = tmem_slot + 3;  // [2] units (e4m3)
 
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
@@ -269,6 +306,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
       mbar_init(&q_raw[i], 1);
+      mbar_init(&wide_full[i], 1);
+      mbar_init(&wide_empty[i], 4);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -296,8 +335,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       volatile uint32_t* refs = reinterpret_cast<volatile uint32_t*>(smem + TileSmem::kRef);
       uint8_t* q_scale = smem + TileSmem::kQScale;
       int it = 0, n_unit[2] = {0, 0};
-      for (int u = u_begin; u < u_end; ++u) {
-        const PagedUnit un = p.units[u];
+      // a unit's tiles; two loops, since the wide one's instructions in the other's loop cost that 35 us of 240 (and the softmax another 30)
+      auto convert = [&](int u, const PagedUnit& un, auto wide_c) {
+        constexpr bool kW = decltype(wide_c)::value;
         for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
           const int s = it & 1;
           const int live = min(kTileKeys, un.key1 - key);
@@ -308,7 +348,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             const uint8_t* scale = smem + TileSmem::kScale + kv * 128;
             uint8_t* dst = (kv ? sV : sK) + s * T32;
             // the tile's largest scale: lane i looks at rows 4i..4i+3; NaN rows and those behind the last key do not count
-            uint32_t top = 0u, low = 255u;
+            uint32_t top = 0u;
+            bool some_nan = false;
             {
               const uint32_t w = reinterpret_cast<const uint32_t*>(scale)[lane];
 #pragma unroll
@@ -316,14 +357,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
                 const uint32_t b = (w >> (8 * i)) & 255u;
                 if (4 * lane + i < live) {
                   if (b != 255u) top = max(top, b);
-                  low = min(low, b == 255u ? 0u : b);
+                  some_nan |= b == 255u;
                 }
               }
             }
-            const uint32_t ref = __reduce_max_sync(0xffffffffu, top);
-            // 0 also where a row is NaN (a signed minimum, or a larger least `ref`, took as long)
-            const uint32_t least = __reduce_min_sync(0xffffffffu, low);
-            const bool near = live == kTileKeys && least != 0u && ref - least <= 14u;
+            const uint32_t ref = kW ? 127u : __reduce_max_sync(0xffffffffu, top);
+            const bool near = live == kTileKeys && !__any_sync(0xffffffffu, some_nan);
             // Pieces 2e and 2e + 1 of a row; lanes of the second 64 dims take the odd one first, so that the eight
             // lanes of a row hit all banks once. All of a tile is read before its place in the ring is waited for.
             uint2 x0[8], x1[8];
@@ -337,13 +376,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
                 x1[i] = *reinterpret_cast<const uint2*>(src + (odd ? 0 : 8) + i * 2048);
                 f[i] = scale[16 * i + sub];
               }
-              if (near) {
+              if constexpr (kW) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = __float_as_uint(e8m0_value(f[i]));
+              } else if (near) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = f[i] * 0x04000400u + base;
               } else {
 #pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = near_factor(f[i], ref);
+              }
+              if (live < kTileKeys) {
+#pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  f[i] = far_factor(f[i], ref);
                   // what lies behind the last key must not reach the sum, whatever it is
                   if (16 * i + sub >= live) {
                     f[i] = 0u;
@@ -353,13 +398,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               }
             }
             mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((it >> 1) & 1) ^ 1u, wg);
-            if (ct == 0) refs[kv * 4 + (it & 3)] = ref;
+            if (ct == 0) refs[kv * 4 + (it & 3)] = ref | (kW && kv == 0 ? kWide : 0u);
             uint8_t* dst0 = dst + tile_offset(sub, 2 * e + (odd ? 1 : 0));
             uint8_t* dst1 = dst + tile_offset(sub, 2 * e + (odd ? 0 : 1));
+            if constexpr (kW) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              *reinterpret_cast<uint4*>(dst0 + i * 2048) = e4m3x8_f16(x0[i], f[i]);
-              *reinterpret_cast<uint4*>(dst1 + i * 2048) = e4m3x8_f16(x1[i], f[i]);
+              for (int i = 0; i < 8; ++i) {
+                *reinterpret_cast<uint4*>(dst0 + i * 2048) = dequant8(x0[i], __uint_as_float(f[i]));
+                *reinterpret_cast<uint4*>(dst1 + i * 2048) = dequant8(x1[i], __uint_as_float(f[i]));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                *reinterpret_cast<uint4*>(dst0 + i * 2048) = e4m3x8_f16(x0[i], f[i]);
+                *reinterpret_cast<uint4*>(dst1 + i * 2048) = e4m3x8_f16(x1[i], f[i]);
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -370,14 +423,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           }
           if (key > un.key0) continue;
           // the unit's queries, in place: |q| / 2^x < 2 for the largest of a row; rows of zeros, of f32 subnormals or
-          // with a value that is not finite as they are
+          // with a value that is not finite as they are, and all of them where the unit is wide
           const int rows = min(kTileRows, un.rows - un.row0);
           for (int t = 0; t * 128 < rows; ++t) {
             mbar_wait(&q_raw[t], n_unit[t] & 1, wg);
             ++n_unit[t];
             uint8_t* qt = sQ + t * T32;
+            if (kW) q_scale[(u & 1) * 256 + t * 128 + ct] = 127u;
 #pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
+            for (int i = kW ? 8 : 0; i < 8; ++i) {
               const int r = 16 * i + sub;
               uint4* pa = reinterpret_cast<uint4*>(qt + tile_offset(r, e));
               uint4* pb = reinterpret_cast<uint4*>(qt + tile_offset(r, 8 + e));
@@ -401,6 +455,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             if (lane == 0) mbar_arrive(&q_full[t]);
           }
         }
+      };
+      for (int u = u_begin; u < u_end; ++u) {
+        const PagedUnit un = p.units[u];
+        const int slot = (u - u_begin) & 1;
+        mbar_wait(&wide_full[slot], ((u - u_begin) >> 1) & 1, wg);
+        const bool wide = wide_flag[slot] != 0u;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wide_empty[slot]);
+        if (wide)
+          convert(u, un, std::true_type{});
+        else
+          convert(u, un, std::false_type{});
       }
     }
   } else if (warp >= 12) {
@@ -508,15 +574,53 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         }
       }
     }
+    if constexpr (kE4m3) {
+      if (warp == 15) {
+        // -------------------------------------------------------- is the unit wide? A unit or two ahead
+        const int ps16 = p.page_shift - 4;
+        for (int u = u_begin; u < u_end; ++u) {
+          const PagedUnit un = p.units[u];
+          const int* pages = p.pages + un.page0;
+          ScaleSpan keys, values;
+          constexpr int kAhead = 4;  // pieces of 16 rows of a lane on their way
+          for (int c0 = (un.key0 >> 4) + lane; c0 * 16 < un.key1; c0 += 32 * kAhead) {
+            uint4 k[kAhead], v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+              const int c = c0 + 32 * i;
+              if (c * 16 < un.key1) {
+                const int row = ((pages[c >> ps16] * p.Hkv + un.head) << p.page_shift) + ((c & ((1 << ps16) - 1)) << 4);
+                k[i] = *reinterpret_cast<const uint4*>(p.pool.ks + row);
+                v[i] = *reinterpret_cast<const uint4*>(p.pool.vs + row);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+              const int rem = un.key1 - (c0 + 32 * i) * 16;
+              if (rem > 0) {
+                keys.take(k[i], rem);
+                values.take(v[i], rem);
+              }
+            }
+          }
+          const bool wide = keys.span() > kKeySpan || values.span() > kValueSpan;
+          const int slot = (u - u_begin) & 1;
+          if (lane == 0) {
+            mbar_wait(&wide_empty[slot], (((u - u_begin) >> 1) & 1) ^ 1u, wg);
+            wide_flag[slot] = wide;
+            mbar_arrive(&wide_full[slot]);
+          }
+          __syncwarp();
+        }
+      }
+    }
     // ------------------------------------------------------------ MMA issue
     if (warp == 12) {
-      constexpr uint32_t idesc_qk = idesc_f16(128, 128, !kE4m3, !kE4m3, false, false);
-      constexpr uint32_t idesc_pv = idesc_f16(128, 128, !kE4m3, !kE4m3, false, true);
       const bool leader = elect_one();
       int it = 0, n_unit[2] = {0, 0}, n_p[2] = {0, 0};  // key tiles; units and key tiles per query tile
       const uint64_t q_desc = kmajor_desc(smem_u32(sQ), 0, 16384), k_desc = kmajor_desc(smem_u32(sK), 0, 16384);
       const uint64_t v_desc = mnmajor_desc(smem_u32(sV), 0, 16384);
-      auto issue_s = [&](int t, int stage, bool last) {
+      auto issue_s = [&](int t, int stage, bool last, uint32_t idesc_qk) {
         const uint64_t qd = q_desc + t * (T32 >> 4), kd = k_desc + stage * (T32 >> 4);
         if (leader) {
 #pragma unroll
@@ -528,8 +632,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           if (last) umma_commit(&q_empty[t]);
         }
       };
-      for (int u = u_begin; u < u_end; ++u) {
-        const PagedUnit un = p.units[u];
+      auto run_unit = [&](const PagedUnit& un, auto bf16_c) {
+        constexpr bool kB = decltype(bf16_c)::value;
+        constexpr uint32_t idesc_qk = idesc_f16(128, 128, kB, kB, false, false);
+        constexpr uint32_t idesc_pv = idesc_f16(128, 128, kB, kB, false, true);
         const int rows = un.rows - un.row0;
         const int nt = rows > 128 ? 2 : 1;
         const int tiles = (un.key1 - un.key0 + kTileKeys - 1) / kTileKeys;
@@ -543,7 +649,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               ++n_unit[t];
               tc_fence_after();
               __syncwarp();
-              issue_s(t, s, tiles == 1);
+              issue_s(t, s, tiles == 1, idesc_qk);
             }
             if (leader) umma_commit(&k_empty[s]);
           }
@@ -572,10 +678,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
                 tc_fence_after();
                 __syncwarp();
               }
-              issue_s(t, s1, j + 2 == tiles);  // overwrites P_t only after the P V MMAs above (in-order issue)
+              issue_s(t, s1, j + 2 == tiles, idesc_qk);  // overwrites P_t only after the P V MMAs above (in-order issue)
               if (leader && t == nt - 1) umma_commit(&k_empty[s1]);
             }
           }
+        }
+      };
+      for (int u = u_begin; u < u_end; ++u) {
+        const PagedUnit un = p.units[u];
+        if constexpr (kE4m3) {
+          mbar_wait(&k_full[it & 1], (it >> 1) & 1, wg);  // the flag stands beside the first key tile's reference
+          if (reinterpret_cast<const volatile uint32_t*>(smem + TileSmem::kRef)[it & 3] & kWide)
+            run_unit(un, std::true_type{});
+          else
+            run_unit(un, std::false_type{});
+        } else {
+          run_unit(un, std::true_type{});
         }
       }
     }
@@ -607,81 +725,97 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       }
       float m_run = -INFINITY, l_run = 0.f;
       float q_factor = p.scale_log2;
-      int v_ref = 0;  // e4m3: largest value scale so far; O counts in units of 2^(v_ref - 127)
-      bool first = true;
-      for (int key = key0; key < key1; key += kTileKeys, ++n_s, ++it) {
-        mbar_wait(&s_full[t], n_s & 1, wg);
-        tc_fence_after();
-        const int valid = limit - key;  // keys of this tile that this row sees
-        // warp-uniform, as the tcgen05 instructions in the branches are
-        const bool full = __all_sync(0xffffffffu, valid >= kTileKeys);
-        uint32_t s[4][32];
+      int v_ref = 0;  // e4m3: largest value scale so far; O counts in units of 2^(v_ref - 127 - kWeightUp), or of 1 (wide)
+      auto run_tiles = [&](auto bf16_c) {
+        constexpr bool kB = decltype(bf16_c)::value;  // operands
+        bool first = true;
+        for (int key = key0; key < key1; key += kTileKeys, ++n_s, ++it) {
+          mbar_wait(&s_full[t], n_s & 1, wg);
+          tc_fence_after();
+          const int valid = limit - key;  // keys of this tile that this row sees
+          // warp-uniform, as the tcgen05 instructions in the branches are
+          const bool full = __all_sync(0xffffffffu, valid >= kTileKeys);
+          uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
-        tmem_ld_wait();
-        if (!full) {
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+          tmem_ld_wait();
+          if (!full) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
-        }
-        const float mx = scores_max(s);
-        float scale = p.scale_log2, v_down = 0.f;
-        bool v_grow = false;
-        if constexpr (kE4m3) {
-          if (first) q_factor *= __uint_as_float(static_cast<uint32_t>((smem + TileSmem::kQScale)[(u & 1) * 256 + t * 128 + row]) << 23);
-          scale = q_factor * e8m0_value(refs[it & 3]);
-          mbar_wait(&v_full[it & 1], (it >> 1) & 1, wg);  // the values' scales; long there but for the first tile
-          const int v_tile = static_cast<int>(refs[4 + (it & 3)]);
-          if (first) v_ref = v_tile;
-          v_grow = v_tile > v_ref;
-          v_down = v_grow ? static_cast<float>(v_ref - v_tile) : 0.f;  // of what O holds
-          v_ref = max(v_ref, v_tile);
-        }
-        float m_tile = mx * scale;
-        if (m_tile == INFINITY) m_tile = NAN;  // infinite scores have no softmax
-        // raised by -inf -> finite, by more than 2^8, and for good by a NaN
-        const bool need = !(m_tile <= m_run + kLazyRescaleLog2);
-        if (__any_sync(0xffffffffu, need) || v_grow) {
-          const float m_new = need ? m_tile : m_run;
-          const float alpha = need ? ex2_approx(m_run - m_new) : 1.f;
-          m_run = m_new;
-          if (!first) {
-            const float o_down = kE4m3 ? alpha * ex2_approx(v_down) : alpha;
-            // S of this tile was issued after the previous P V, which is therefore complete
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint32_t r[16];
-              tmem_ld16(tO + c * 16, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * o_down);
-              tmem_st16(tO + c * 16, r);
-            }
-            l_run *= alpha;
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
           }
-        }
-        first = false;
-        float neg_m = -finite_or_zero(m_run), p_up = 1.f;
-        if constexpr (kE4m3) {
-          // weights relative to the largest value scale; the row sum without it
-          const float d = fmaxf(static_cast<float>(static_cast<int>(refs[4 + (it & 3)]) - v_ref), -100.f);
-          neg_m += d;
-          p_up = ex2_approx(-d);
-        }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float mx = scores_max(s);
+          float scale = p.scale_log2, v_down = 0.f;
+          bool v_grow = false;
+          if constexpr (kE4m3) {
+            if (first) q_factor *= __uint_as_float(static_cast<uint32_t>((smem + TileSmem::kQScale)[(u & 1) * 256 + t * 128 + row]) << 23);
+            scale = q_factor * e8m0_value(refs[it & 3] & 255u);
+          }
+          if constexpr (!kB) {
+            mbar_wait(&v_full[it & 1], (it >> 1) & 1, wg);  // the values' scales; long there but for the first tile
+            const int v_tile = static_cast<int>(refs[4 + (it & 3)]);
+            if (first) v_ref = v_tile;
+            v_grow = v_tile > v_ref;
+            v_down = v_grow ? static_cast<float>(v_ref - v_tile) : 0.f;  // of what O holds
+            v_ref = max(v_ref, v_tile);
+          }
+          float m_tile = mx * scale;
+          if (m_tile == INFINITY) m_tile = NAN;  // infinite scores have no softmax
+          // raised by -inf -> finite, by more than 2^8, and for good by a NaN
+          const bool need = !(m_tile <= m_run + kLazyRescaleLog2);
+          if (__any_sync(0xffffffffu, need) || v_grow) {
+            const float m_new = need ? m_tile : m_run;
+            const float alpha = need ? ex2_approx(m_run - m_new) : 1.f;
+            m_run = m_new;
+            if (!first) {
+              const float o_down = kB ? alpha : alpha * ex2_approx(v_down);
+              // S of this tile was issued after the previous P V, which is therefore complete
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+              for (int c = 0; c < 8; ++c) {
+                uint32_t r[16];
+                tmem_ld16(tO + c * 16, r);
+                tmem_ld_wait();
 #pragma unroll
-          for (int c = 2 * half; c < 2 * half + 2; ++c) scores_exp32<!kE4m3>(s[c], tS + c * 16, scale, neg_m, sum);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * o_down);
+                tmem_st16(tO + c * 16, r);
+              }
+              l_run *= alpha;
+            }
+          }
+          first = false;
+          float neg_m = -finite_or_zero(m_run), p_up = 1.f;
+          if constexpr (!kB) {
+            // weights relative to the largest value scale; the row sum without it
+            const float up = fmaxf(static_cast<float>(static_cast<int>(refs[4 + (it & 3)]) - v_ref), -100.f) + kWeightUp;
+            neg_m += up;
+            p_up = ex2_approx(-up);
+          }
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int c = 2 * half; c < 2 * half + 2; ++c) scores_exp32<kB>(s[c], tS + c * 16, scale, neg_m, sum);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+          }
+          const float tile_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l_run = kB ? l_run + tile_sum : fmaf(tile_sum, p_up, l_run);
         }
-        const float tile_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        l_run = kE4m3 ? fmaf(tile_sum, p_up, l_run) : l_run + tile_sum;
+      };
+      bool wide = false;
+      if constexpr (kE4m3) {
+        mbar_wait(&s_full[t], n_s & 1, wg);
+        wide = (refs[it & 3] & kWide) != 0u;
+        if (wide)
+          run_tiles(std::true_type{});
+        else
+          run_tiles(std::false_type{});
+      } else {
+        run_tiles(std::true_type{});
       }
       mbar_wait(&o_full[t], n_unit & 1, wg);
       ++n_unit;
@@ -695,7 +829,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       };
       const int nsplit = un.split >> 16, split = un.split & 0xffff;
       const float inv_l = nsplit == 1 ? 1.0f / l_run : 1.0f;
-      const float unit_v = kE4m3 ? e8m0_value(static_cast<uint32_t>(v_ref)) : 1.0f;
+      const float unit_v = kE4m3 && !wide ? e8m0_value(static_cast<uint32_t>(v_ref)) * 0.0078125f : 1.0f;  // 2^-kWeightUp
       const float inv = inv_l * unit_v;
       const long long orow = out_row_of(min(t * 128 + row, unit_rows - 1));
       float* slot = p.part + static_cast<long long>(un.slot0 + split) * kTileSlot;

@@ -44,11 +44,11 @@ def check_rows(paged, pool, table, q, q_len, kv_len, visible, o, lse, small=smal
         assert np.all(np.abs(lse[i:i + 1] - l) <= lse_tolerance(l, mag)), (i, lse[i], l)
 
 
-# 4 query heads over 2 KV heads: 2 or 3 tokens are 4 or 6 query rows of a unit of 8
+# 4 query heads over 2 KV heads: 2 or 3 tokens are 4 or 6 query rows of a unit of 8, 200 tokens 400 rows of two of 256
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("what", ["k", "v"])
-@pytest.mark.parametrize("power", [10, 17, 24, 30, 60])
-@pytest.mark.parametrize("q_len,past,where", [(2, 0, 1), (3, 300, 2), (4, 61, 1)])
+@pytest.mark.parametrize("power", [10, 17, 24, 30])
+@pytest.mark.parametrize("q_len,past,where", [(2, 0, 1), (3, 300, 2), (4, 61, 1), (200, 0, 1), (200, 70, 130), (130, 300, 129)])
 def test_rows_that_a_query_does_not_see_may_be_of_any_size(cuda_ready, q_len, past, where, power, what, kv):
     g = torch.Generator().manual_seed(q_len + power)
     n = past + q_len
@@ -63,7 +63,7 @@ def test_rows_that_a_query_does_not_see_may_be_of_any_size(cuda_ready, q_len, pa
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("power", [20, 40, 90])
 @pytest.mark.parametrize("big_first", [False, True])
-@pytest.mark.parametrize("q_len,n", [(1, 40), (3, 700)])
+@pytest.mark.parametrize("q_len,n", [(1, 40), (3, 700), (40, 90), (130, 700)])
 def test_a_large_value_of_small_weight_leaves_the_others(cuda_ready, q_len, n, big_first, power, kv):
     # Half of the keys have score 22.6 and values of 1, the others score -22.6 (weights of 2^-65) and values of 2^power:
     # all of them seen by all queries. A weight that meets 8-bit values is a multiple of 2^-31 of the largest product of
@@ -85,3 +85,56 @@ def test_a_large_value_of_small_weight_leaves_the_others(cuda_ready, q_len, n, b
         w = np.exp(s - 22.6)
         return len(w) * 2.0 ** -31 * (w / w.sum() * np.abs(vv).max(-1)).max() if kv_dtype == "e4m3" else 0.0
     check_rows(paged, pool, table, q, q_len, n, n, o, lse, small=small, rows=sorted({0, q_len // 2, q_len - 1}))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [24, 60])
+@pytest.mark.parametrize("q_len", [1, 100])
+def test_keys_far_apart_keep_their_scores(cuda_ready, q_len, power, kv):
+    # One seen key is 2^power times the others and at right angles to the queries (score 0 exactly): the scores of the
+    # others count, and the bound on them does not have the large key's size in it.
+    g = torch.Generator().manual_seed(power)
+    n = 150
+    k, v = (torch.randn(1, 2, n, 128, generator=g) for _ in range(2))
+    k[0, :, 20, :64] = 0
+    k[0, :, 20] *= 2.0 ** power
+    paged, pool, table, batch = cached(4, 2, 16, kv, [q_len], [n], k, v, visible=[n])
+    q = torch.randn(q_len, 4, 128, generator=g)
+    q[..., 64:] = 0
+    q = q.to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+    kk, vv = (sequence_rows(x, table, 0, n, 16) for x in pool_values(pool))
+    kk[:, 20] = 0  # the same scores
+    ref, l, absv, mag = PG.chunk_attention(as_f64(q), kk, vv, n)
+    assert np.all(np.abs(o - ref) <= attend_tolerance(ref, absv, mag, small_weights(kv, vv)))
+    assert np.all(np.abs(lse - l) <= lse_tolerance(l, mag))
+
+
+@pytest.mark.parametrize("hq,hkv,page", [(4, 2, 16), (4, 4, 128), (6, 2, 64), (8, 1, 32)])
+def test_units_of_both_kinds_in_turn(cuda_ready, hq, hkv, page):
+    # many sequences a CTA, every other one with scales that f16 does not bear (large or small values or keys, rows of
+    # zeros), lengths that end inside a tile, one row of NaN that only the last query of its sequence sees
+    g = torch.Generator().manual_seed(hq)
+    lengths = [200, 129, 300, 70, 257, 512, 90, 385] * 8
+    q_len = [70, 129, 40, 70, 100, 33, 90, 260] * 8
+    n, rows = len(lengths), max(lengths)
+    k, v = (torch.randn(n, hkv, rows, 128, generator=g) for _ in range(2))
+    for b in range(0, n, 2):
+        at = torch.randint(0, lengths[b], (7,), generator=g)
+        (v if b % 4 else k)[b, :, at] *= 2.0 ** (20 if b % 8 else -30)
+    for b in range(1, n, 8):
+        v[b, :, lengths[b] // 2] = 0
+    v[5, :, lengths[5] - 1, 3] = float("nan")
+    paged, pool, table, batch = cached(hq, hkv, page, "e4m3", q_len, lengths, k, v)
+    q = torch.randn(sum(q_len), hq, 128, generator=g).to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+    at = 0
+    for b in range(n):
+        sl = slice(at, at + q_len[b])
+        if b < 16 or b % 7 == 0:
+            last = q_len[b] - 1
+            check_rows(paged, pool, table[b:b + 1], q[sl], q_len[b], lengths[b], 0, o[sl], lse[sl],
+                       rows=[0, q_len[b] // 2, last - (b == 5)])
+        at += q_len[b]
+    end = sum(q_len[:6]) - 1
+    assert np.isnan(o[end]).all() and np.isfinite(o[:end]).all() and np.isfinite(o[end + 1:]).all()
