@@ -118,6 +118,10 @@ constexpr int kKeySpan = 14, kValueSpan = 7;
 constexpr float kWeightUp = 7.f;  // weights of f16 units are 2^kWeightUp times as large
 constexpr uint32_t kWide = 256u;
 
+// Running max from which on it is not subtracted from the scores in one fused step: what the max lost when it was
+// rounded, up to 2^-24 of it, would be left in every exponent. Such scores are rounded by themselves first.
+constexpr float kFarScore = 1048576.f;
+
 // largest and smallest scale byte of `rem` rows from `src` on (16 at most); 255 (NaN) counts as neither
 struct ScaleSpan {
   uint32_t top = 0u, low = 0x00ff00ffu;  // pairs; top: plus 1, 0 = none
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       int v_ref = 0;  // e4m3: largest value scale so far; O counts in units of 2^(v_ref - 127 - kWeightUp), or of 1 (wide)
       auto run_tiles = [&](auto bf16_c) {
         constexpr bool kB = decltype(bf16_c)::value;  // operands
-        bool first = true;
+        bool first = true, far = false;
         for (int key = key0; key < key1; key += kTileKeys, ++n_s, ++it) {
           mbar_wait(&s_full[t], n_s & 1, wg);
           tc_fence_after();
@@ -769,6 +773,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             const float m_new = need ? m_tile : m_run;
             const float alpha = need ? ex2_approx(m_run - m_new) : 1.f;
             m_run = m_new;
+            far = __any_sync(0xffffffffu, fabsf(m_run) >= kFarScore && m_run > -INFINITY);
             if (!first) {
               const float o_down = kB ? alpha : alpha * ex2_approx(v_down);
               // S of this tile was issued after the previous P V, which is therefore complete
@@ -786,6 +791,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           }
           first = false;
           float neg_m = -finite_or_zero(m_run), p_up = 1.f;
+          if (far) {
+            // Through TMEM and rolled up, to stay out of the loop's way. All rows of the warp take part.
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t r[16];
+              tmem_ld16(tS + c * 16, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                r[i] = c * 16 + i >= valid ? __float_as_uint(-INFINITY)
+                                           : __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(r[i]), scale), neg_m));
+              tmem_st16(tS + c * 16, r);
+            }
+            tmem_st_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
+            tmem_ld_wait();
+            scale = 1.f;
+            neg_m = 0.f;
+          }
           if constexpr (!kB) {
             // weights relative to the largest value scale; the row sum without it
             const float up = fmaxf(static_cast<float>(static_cast<int>(refs[4 + (it & 3)]) - v_ref), -100.f) + kWeightUp;

@@ -47,7 +47,7 @@ def check_rows(paged, pool, table, q, q_len, kv_len, visible, o, lse, small=smal
 # 4 query heads over 2 KV heads: 2 or 3 tokens are 4 or 6 query rows of a unit of 8, 200 tokens 400 rows of two of 256
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("what", ["k", "v"])
-@pytest.mark.parametrize("power", [10, 17, 24, 30])
+@pytest.mark.parametrize("power", [10, 17, 24, 30, 60])
 @pytest.mark.parametrize("q_len,past,where", [(2, 0, 1), (3, 300, 2), (4, 61, 1), (200, 0, 1), (200, 70, 130), (130, 300, 129)])
 def test_rows_that_a_query_does_not_see_may_be_of_any_size(cuda_ready, q_len, past, where, power, what, kv):
     g = torch.Generator().manual_seed(q_len + power)
