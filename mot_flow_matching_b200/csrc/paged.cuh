@@ -56,6 +56,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// Biased exponent x of the power of two that a query row with largest magnitude
+// amax is divided by to be held in f16: amax / 2^(x - 127) < 4, both 2^(x - 127) and
+// its inverse normal f32. A row that is not finite stays as it is.
+__device__ __forceinline__ uint32_t query_exponent(float amax) {
+  const uint32_t x = (__float_as_uint(amax) >> 23) & 255u;
+  return x == 255u ? 127u : min(max(x, 1u), 253u);
+}
+
 __device__ __forceinline__ void unpack_bf16x8(const uint4& w, float (&f)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -678,11 +686,8 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
         }
         m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.f);
         m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, 2), 0.f);
-        // 2^x with |q| / 2^x < 2; rows of zeros, of f32 subnormals or with a non-finite value stay as they are
-        const uint32_t ex = (__float_as_uint(m) >> 23) & 255u;
-        const bool plain = ex == 0u || ex == 255u;
-        const float down = plain ? 1.f : __uint_as_float(max(1u, 254u - ex) << 23);
-        const float up = plain ? 1.f : __uint_as_float(ex << 23);
+        const uint32_t ex = query_exponent(m);
+        const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
 #pragma unroll
         for (int i = 0; i < 16; ++i) q[i] = pack_half2(f[i >> 2][2 * (i & 3)] * down, f[i >> 2][2 * (i & 3) + 1] * down);
         qf[0] *= __shfl_sync(0xffffffffu, up, 8 * c);      // row 2c is lane group g = 2c

@@ -426,8 +426,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
             }
           }
           if (key > un.key0) continue;
-          // the unit's queries, in place: |q| / 2^x < 2 for the largest of a row; rows of zeros, of f32 subnormals or
-          // with a value that is not finite as they are, and all of them where the unit is wide
+          // the unit's queries, in place: |q| / 2^x < 4 for the largest of a row; as they are where the unit is wide
           const int rows = min(kTileRows, un.rows - un.row0);
           for (int t = 0; t * 128 < rows; ++t) {
             mbar_wait(&q_raw[t], n_unit[t] & 1, wg);
@@ -445,10 +444,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               float m = fmax3_nan(amax8(a), amax8(b), 0.f);
 #pragma unroll
               for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
-              const uint32_t ex = (__float_as_uint(m) >> 23) & 255u;
-              const bool plain = ex == 0u || ex == 255u;
-              const float down = plain ? 1.f : __uint_as_float(max(1u, 254u - ex) << 23);
-              if (e == 0) q_scale[(u & 1) * 256 + t * 128 + r] = static_cast<uint8_t>(plain ? 127u : ex);
+              const uint32_t ex = query_exponent(m);
+              const float down = __uint_as_float((254u - ex) << 23);
+              if (e == 0) q_scale[(u & 1) * 256 + t * 128 + r] = static_cast<uint8_t>(ex);
               *pa = make_uint4(pack_half2(a[0] * down, a[1] * down), pack_half2(a[2] * down, a[3] * down),
                                pack_half2(a[4] * down, a[5] * down), pack_half2(a[6] * down, a[7] * down));
               *pb = make_uint4(pack_half2(b[0] * down, b[1] * down), pack_half2(b[2] * down, b[3] * down),

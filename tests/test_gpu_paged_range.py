@@ -1,6 +1,7 @@
 """The paged attention over its whole range of magnitudes: cached rows of very
-different size, seen and unseen. Every query is held to the fp64 oracle over the
-keys that it sees, and every bound is taken from those keys alone."""
+different size, seen and unseen, queries near the ends of f32. Every query is
+held to the fp64 oracle over the keys that it sees, and every bound is taken
+from those keys alone."""
 import numpy as np
 import pytest
 import torch
@@ -138,3 +139,36 @@ def test_units_of_both_kinds_in_turn(cuda_ready, hq, hkv, page):
         at += q_len[b]
     end = sum(q_len[:6]) - 1
     assert np.isnan(o[end]).all() and np.isfinite(o[:end]).all() and np.isfinite(o[end + 1:]).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len", [1, 60])
+def test_queries_of_the_largest_size(cuda_ready, q_len, kv):
+    # magnitudes of 2^127 over small keys, one of a row's 128 products not zero: the scores are finite
+    n = 60
+    g = torch.Generator().manual_seed(1)
+    k, v = torch.zeros(1, 2, n, 128), torch.randn(1, 2, n, 128, generator=g)
+    k[..., 5] = 2.0 ** -60
+    paged, pool, table, batch = cached(4, 2, 16, kv, [q_len], [n], k, v)
+    q = torch.zeros(q_len, 4, 128)
+    q[:, :, 5] = 1.5 * 2.0 ** 127
+    q[:, 1, 5] = 2.0 ** 126
+    q[:, 3, 5] = -2.0 ** 127
+    q = q.to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+    check_rows(paged, pool, table, q, q_len, n, 0, o, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len", [1, 3, 150])
+@pytest.mark.parametrize("power", [-50, 60, 110, 125, 127])
+def test_small_queries_over_large_keys_and_the_reverse(cuda_ready, q_len, power, kv):
+    # queries of 2^-power over keys of 2^(power - 2): scores of order 1 from factors at either end of f32 (2^-127 is a
+    # subnormal)
+    n = 180
+    g = torch.Generator().manual_seed(power)
+    k, v = torch.randn(1, 2, n, 128, generator=g).clamp(-2.5, 2.5) * 2.0 ** (power - 2), torch.randn(1, 2, n, 128, generator=g)
+    paged, pool, table, batch = cached(4, 2, 16, kv, [q_len], [n], k, v)
+    q = (torch.randn(q_len, 4, 128, generator=g).double() * 2.0 ** -power).to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+    check_rows(paged, pool, table, q, q_len, n, 0, o, lse, rows=sorted({0, q_len // 2, q_len - 1}))
