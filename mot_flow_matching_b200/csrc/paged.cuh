@@ -3,6 +3,7 @@
 // attention of few query rows per sequence over the pages.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -745,8 +746,14 @@ paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {
               mma_16816<false>(s[h & 1], a0, b0, a1, b1, q[8 * i + 2 * h], q[8 * i + 2 * h + 1]);
             }
           }
+          const float top = fmaxf(qf[0], qf[1]) * fmaxf(kf[0], kf[1]);
+          if (top <= FLT_MAX) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = (s[0][i] + s[1][i]) * (qf[i & 1] * kf[i >> 1]);
+            for (int i = 0; i < 4; ++i) x[i] = (s[0][i] + s[1][i]) * (qf[i & 1] * kf[i >> 1]);
+          } else {  // their product may be infinite though the score is not
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = (s[0][i] + s[1][i]) * qf[i & 1] * kf[i >> 1];
+          }
         }
         const Unseen unseen{min(lim_max, un.key1) - key, key, lim_max != lim_min, s_poison};
         if (!whole) {

@@ -114,7 +114,10 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
 // units of 2^kValueSpan of a row with a largest value of at least 224: 2^-24 of
 // the largest value that a query sees, a key, whatever the size of those that it
 // does not see). Wide units run on bf16 operands, which hold every row as it is.
+// So do units with a key scale above 2^(kKeyTop - 127): below it the factor of a row's
+// scores, at most 2^123 from the query's side, is an f32.
 constexpr int kKeySpan = 14, kValueSpan = 7;
+constexpr int kKeyTop = 131;
 constexpr float kWeightUp = 7.f;  // weights of f16 units are 2^kWeightUp times as large
 constexpr uint32_t kWide = 256u;
 
@@ -136,11 +139,11 @@ struct ScaleSpan {
       low = __vminu2(low, __vminu2(a, b));
     }
   }
-  // over the warp: largest minus smallest; negative when there is none
-  __device__ __forceinline__ int span() const {
-    const uint32_t t = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-    const uint32_t l = __reduce_min_sync(0xffffffffu, min(low & 0xffffu, low >> 16));
-    return static_cast<int>(t) - 1 - static_cast<int>(l);
+  // over the warp: whether the largest is more than `most`, or more than `span` above the smallest
+  __device__ __forceinline__ bool beyond(int span, int most) const {
+    const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16))) - 1;
+    const int l = static_cast<int>(__reduce_min_sync(0xffffffffu, min(low & 0xffffu, low >> 16)));
+    return t > most || t - l > span;
   }
 };
 
@@ -605,11 +608,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               }
             }
           }
-          const bool wide = keys.span() > kKeySpan || values.span() > kValueSpan;
+          const bool key_wide = keys.beyond(kKeySpan, kKeyTop), value_wide = values.beyond(kValueSpan, 255);
           const int slot = (u - u_begin) & 1;
           if (lane == 0) {
             mbar_wait(&wide_empty[slot], (((u - u_begin) >> 1) & 1) ^ 1u, wg);
-            wide_flag[slot] = wide;
+            wide_flag[slot] = key_wide || value_wide;
             mbar_arrive(&wide_full[slot]);
           }
           __syncwarp();
@@ -753,7 +756,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           bool v_grow = false;
           if constexpr (kE4m3) {
             if (first) q_factor *= __uint_as_float(static_cast<uint32_t>((smem + TileSmem::kQScale)[(u & 1) * 256 + t * 128 + row]) << 23);
-            scale = q_factor * e8m0_value(refs[it & 3] & 255u);
+            // at least 2^-126: as good as 0 for scores, and -infinity times it is -infinity
+            scale = fmaxf(q_factor * e8m0_value(refs[it & 3] & 255u), FLT_MIN);
           }
           if constexpr (!kB) {
             mbar_wait(&v_full[it & 1], (it >> 1) & 1, wg);  // the values' scales; long there but for the first tile

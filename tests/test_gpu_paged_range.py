@@ -160,6 +160,24 @@ def test_queries_of_the_largest_size(cuda_ready, q_len, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len", [1, 3, 200])
+@pytest.mark.parametrize("q_power,k_power", [(-100, None), (-120, None), (-90, -60), (100, 60), (126, 100), (60, 110)])
+def test_scores_of_zero_from_factors_of_any_size(cuda_ready, q_len, q_power, k_power, kv):
+    # keys of zeros (k_power None) or at right angles to the queries: every score is 0, the output the mean of the values
+    n = 230
+    g = torch.Generator().manual_seed(2)
+    k, v = torch.zeros(1, 2, n, 128), torch.randn(1, 2, n, 128, generator=g)
+    if k_power is not None:
+        k[..., 64:] = torch.randn(1, 2, n, 64, generator=g) * 2.0 ** k_power
+    paged, pool, table, batch = cached(4, 2, 16, kv, [q_len], [n], k, v)
+    q = torch.zeros(q_len, 4, 128)
+    q[..., :64] = torch.rand(q_len, 4, 64, generator=g) * 2.0 ** q_power
+    q = q.to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+    check_rows(paged, pool, table, q, q_len, n, 0, o, lse, rows=sorted({0, q_len // 2, q_len - 1}))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("q_len", [1, 3, 150])
 @pytest.mark.parametrize("power", [-50, 60, 110, 125, 127])
 def test_small_queries_over_large_keys_and_the_reverse(cuda_ready, q_len, power, kv):
@@ -172,3 +190,21 @@ def test_small_queries_over_large_keys_and_the_reverse(cuda_ready, q_len, power,
     q = (torch.randn(q_len, 4, 128, generator=g).double() * 2.0 ** -power).to(torch.bfloat16).cuda()
     o, lse = attend(paged, pool, batch, q)
     check_rows(paged, pool, table, q, q_len, n, 0, o, lse, rows=sorted({0, q_len // 2, q_len - 1}))
+
+
+@pytest.mark.parametrize("q_len", [200, 2])
+def test_small_queries_beside_a_tile_of_nan_scales(cuda_ready, q_len):
+    # keys 128.. have the NaN scale: queries of 2^-30 that see none of them, in one unit with some that do, get the
+    # answer of the others
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(1, 2, 256, 128, generator=g) for _ in range(2))
+    paged, pool, table, batch = cached(4, 2, 16, "e4m3", [q_len], [256], k, v)
+    for i in table[0][8:16]:
+        pool.k_scale.view(torch.uint8)[int(i)] = 255
+        pool.v_scale.view(torch.uint8)[int(i)] = 255
+    q = (torch.randn(q_len, 4, 128, generator=g) * 2.0 ** -30).to(torch.bfloat16).cuda()
+    o, lse = attend(paged, pool, batch, q)
+    free = max(0, q_len - 128)
+    assert np.isnan(o[free:]).all() and np.isnan(lse[free:]).all()
+    if free:
+        check_rows(paged, pool, table, q, q_len, 256, 0, o, lse, rows=[0, 1, 40, free - 1])
