@@ -23,6 +23,10 @@
 // Where a unit's scales lie too far apart for that (`kKeySpan`, `kValueSpan`; warp
 // 15 reads them a unit or two ahead), the operand tiles are bf16 instead, which
 // holds payload times scale, and the queries, as they are.
+// Scores of unseen keys become -infinity. Their values meet weights of zero, so in
+// tiles that not all rows of a unit see warps 8-11 take out what is not finite,
+// and rows that do see it get NaN in those dims at the end (bf16 pages go through
+// these warps only there and at the last key).
 // The registers are split by setmaxnreg: 2 x 192 + 2 x 64 (e4m3: 176 and 80) of
 // the 4 x 128 a thread that the block starts with.
 //
@@ -43,7 +47,8 @@
 // and slower: a quarter of the exponentials by polynomial (image 564 against 555
 // us, a mixed e4m3 batch 289 against 269), a second MMA warp (image 565 against
 // 552), e4m3 conversion on eight warps with fewer registers for the softmax (the
-// mixed batch 272 against 251; 248 now, 239 before wide units were told apart).
+// mixed batch 272 against 251; 251 now, 239 before wide units, large scores and
+// values that are not finite were dealt with in it).
 #pragma once
 
 #include "paged.cuh"
@@ -71,7 +76,8 @@ struct TileSmem {
   static constexpr uint32_t kK = kQ + 2 * kTile;
   static constexpr uint32_t kV = kK + 2 * kTile;
   static constexpr uint32_t kBar = kV + 2 * kTile;
-  static constexpr uint32_t kRaw = kBar + 512;  // e4m3: [keys, values] 128 rows of 128 bytes, then 2 x 128 scales
+  static constexpr uint32_t kPoison = kBar + 512;  // per dim: first key of the unit whose value is not finite
+  static constexpr uint32_t kRaw = kPoison + 512;  // e4m3: [keys, values] 128 rows of 128 bytes, then 2 x 128 scales
   static constexpr uint32_t kRawTile = 16384;
   static constexpr uint32_t kScale = kRaw + 2 * kRawTile;
   static constexpr uint32_t kRef = kScale + 256;   // e4m3: largest scale bytes, keys [4 tiles] (| kWide), values [4 tiles]
@@ -218,49 +224,31 @@ __device__ __forceinline__ void store_row32(uint4* dst, const uint32_t (&r)[32],
   }
 }
 
-// One value of a cached row as f32.
-template <bool kE4m3>
-__device__ __forceinline__ float4 cached4(const uint8_t* pages, const uint8_t* scales, long long row, int lane) {
-  if (kE4m3) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(pages + row * 128)[lane];
-    const float s = e8m0_value(scales[row]);
-    const uint32_t lo = e4m3x2_f16x2(w), hi = e4m3x2_f16x2(w >> 16);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
-  }
-  const uint2 w = reinterpret_cast<const uint2*>(pages + row * 256)[lane];
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
+// Keys that every row of a unit sees: those behind may meet a weight of zero.
+__device__ __forceinline__ int seen_by_all(const PagedUnit& un, int group) {
+  return max(un.vis, un.past + un.row0 / group + 1);
 }
 
-// The sum over keys [key0, limit) of 2^(score - m) V for one query row, by one
-// warp, lane holding dims 4 lane..: for a row whose tensor-core sum met an
-// infinity or NaN in a value that the row does not see (weight zero times
-// infinity). Slow, and only ever run on such values.
-template <bool kE4m3>
-__device__ __noinline__ float4 row_sum_seen(const PagedAttnParams& p, const int* pages, int head, const uint2* q_row, int key0,
-                                            int limit, float m) {
-  const int lane = lane_id();
-  const uint2 w = q_row[lane];
-  const float4 q = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int key = key0; key < limit; ++key) {
-    const long long row = ((static_cast<long long>(pages[key >> p.page_shift]) * p.Hkv + head) << p.page_shift) +
-                          (key & ((1 << p.page_shift) - 1));
-    const float4 k = cached4<kE4m3>(p.pool.k, p.pool.ks, row, lane);
-    float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+// Eight values (16 bits each) of one key, dims d..: zero times an infinity or NaN
+// would reach the rows that do not see the key, so what is not finite becomes zero,
+// and its key is remembered per dim; rows that see it get NaN at the end.
+template <bool kBf16>
+__device__ __forceinline__ void clean8(uint4* at, int key, int d, int* poison, volatile uint32_t* poisoned) {
+  constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
+  uint4 v = *at;
+  const uint32_t all_ones = (((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne)) & 0x80008000u;
+  if (all_ones == 0u) return;
+  *poisoned = 1u;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float e = ex2_approx(fmaf(s, p.scale_log2, -m));
-    const float4 v = cached4<kE4m3>(p.pool.v, p.pool.vs, row, lane);
-    acc.x = fmaf(e, v.x, acc.x);
-    acc.y = fmaf(e, v.y, acc.y);
-    acc.z = fmaf(e, v.z, acc.z);
-    acc.w = fmaf(e, v.w, acc.w);
+  for (int i = 0; i < 8; ++i) {
+    const int sh = 16 * (i & 1);
+    if ((((w[i >> 1] & kExp) + kOne) >> sh) & 0x8000u) {
+      atomicMin(poison + d + i, key);
+      w[i >> 1] &= ~(0xffffu << sh);
+    }
   }
-  return acc;
+  *at = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <bool kE4m3>
@@ -281,17 +269,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   uint64_t* s_full = bars + 10;   // [2] query tiles
   uint64_t* p_full = bars + 12;   // [2 tiles][2 halves of the keys]
   uint64_t* o_full = bars + 16;   // [2]
-  uint64_t* v_raw = bars + 18;    // values of a tile whose tail is still to be cleared
-  uint64_t* q_empty = bars + 19;  // [2]
-  uint64_t* raw_full = bars + 21;   // [2] keys, values (e4m3)
-  uint64_t* raw_empty = bars + 23;  // [2]
-  uint64_t* q_raw = bars + 25;      // [2] query tiles before their conversion (e4m3)
-  uint64_t* wide_full = bars + 27;   // [2] units: whether the unit is wide (e4m3)
-  uint64_t* wide_empty = bars + 29;  // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
+  uint64_t* q_empty = bars + 18;  // [2]
+  uint64_t* raw_full = bars + 20;   // [2] keys, values (e4m3)
+  uint64_t* raw_empty = bars + 22;  // [2]
+  uint64_t* q_raw = bars + 24;      // [2] query tiles before their conversion (e4m3)
+  uint64_t* wide_full = bars + 26;   // [2] units: whether the unit is wide (e4m3)
+  uint64_t* wide_empty = bars + 28;  // [2]
+  uint64_t* v_raw = bars + 30;       // [2] values that are still to be cleaned (bf16)
+  uint64_t* poison_empty = bars + 32;  // [2] query tiles: `poison` read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 34);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* last_flag = tmem_slot + 2;
   volatile uint32_t* wide_flag = tmem_slot + 3;  // [2] units (e4m3)
+  volatile uint32_t* poisoned = tmem_slot + 5;   // some value of the unit was taken out
+  int* poison = reinterpret_cast<int*>(smem + TileSmem::kPoison);
 
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
@@ -306,7 +297,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
     }
-    mbar_init(v_raw, 1);
     mbar_init(&q_empty[0], 1);
     mbar_init(&q_empty[1], 1);
     for (int i = 0; i < 2; ++i) {
@@ -315,6 +305,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       mbar_init(&q_raw[i], 1);
       mbar_init(&wide_full[i], 1);
       mbar_init(&wide_empty[i], 4);
+      mbar_init(&v_raw[i], 1);
+      mbar_init(&poison_empty[i], 4);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -334,132 +326,192 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 
   if (warp >= 8 && warp < 12) {
     regs_down<kE4m3 ? 80 : 64>();
-    if constexpr (kE4m3) {
+    // eight lanes a row, four rows a warp at a time; lane e has pieces 2e and 2e + 1, those of the second 64 dims take
+    // the odd one first, so that the eight lanes of a row hit all banks once
+    const int ct = threadIdx.x - 8 * 32, sub = ct >> 3, e = ct & 7;
+    const bool odd = e >= 4;
+    const int piece0 = 2 * e + (odd ? 1 : 0), piece1 = 2 * e + (odd ? 0 : 1);
+    int n_masked[2] = {0, 0};  // units that a query tile has read `poison` of
+    // the values in a ring tile from `key` on, some of whose keys not all of the unit's rows see; `first`: of the unit
+    auto clean = [&](uint8_t* tile, int key, int live, bool first, int rows, auto bf16_c) {
+      if (first) {
+        mbar_wait(&poison_empty[0], (n_masked[0] & 1) ^ 1u, wg);
+        mbar_wait(&poison_empty[1], (n_masked[1] & 1) ^ 1u, wg);
+        ++n_masked[0];
+        if (rows > 128) ++n_masked[1];
+        poison[ct] = INT_MAX;
+        if (ct == 0) *poisoned = 0u;
+        named_bar_sync(2, 128);
+      }
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {
+        const int r = 16 * i + sub;
+        if (r >= live) break;
+        clean8<decltype(bf16_c)::value>(reinterpret_cast<uint4*>(tile + tile_offset(r, piece0)), key + r, 8 * piece0, poison, poisoned);
+        clean8<decltype(bf16_c)::value>(reinterpret_cast<uint4*>(tile + tile_offset(r, piece1)), key + r, 8 * piece1, poison, poisoned);
+      }
+    };
+    if constexpr (!kE4m3) {
+      // ---------------------------------------------------------- values on their way to the MMAs that some row must not meet
+      int it = 0, n_raw[2] = {0, 0};
+      for (int u = u_begin; u < u_end; ++u) {
+        const PagedUnit un = p.units[u];
+        const int all = seen_by_all(un, p.group);
+        for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
+          const int s = it & 1, live = min(kTileKeys, un.key1 - key);
+          if (live == kTileKeys && key + kTileKeys <= all) continue;
+          mbar_wait(&v_raw[s], n_raw[s] & 1, wg);
+          ++n_raw[s];
+          uint8_t* tile = sV + s * T32;
+          if (key + live > all) clean(tile, key, live, key - kTileKeys < un.key0 || key <= all, un.rows - un.row0, std::true_type{});
+          // what lies behind the last key must not reach the sum, whatever it is: zero
+          for (int r = sub; r < kTileKeys; r += 16)
+            if (r >= live) {
+              *reinterpret_cast<uint4*>(tile + tile_offset(r, piece0)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(tile + tile_offset(r, piece1)) = make_uint4(0, 0, 0, 0);
+            }
+          fence_proxy_async_smem();
+          named_bar_sync(2, 128);
+          if (ct == 0) mbar_arrive(&v_full[s]);
+        }
+      }
+    } else {
       // ---------------------------------------------------------- e4m3 pages, bf16 queries -> f16 operand tiles
-      // eight lanes a row, four rows a warp at a time
-      const int ct = threadIdx.x - 8 * 32, sub = ct >> 3, e = ct & 7;
-      const bool odd = e >= 4;
       volatile uint32_t* refs = reinterpret_cast<volatile uint32_t*>(smem + TileSmem::kRef);
       uint8_t* q_scale = smem + TileSmem::kQScale;
       int it = 0, n_unit[2] = {0, 0};
-      // a unit's tiles; two loops, since the wide one's instructions in the other's loop cost that 35 us of 240 (and the softmax another 30)
-      auto convert = [&](int u, const PagedUnit& un, auto wide_c) {
-        constexpr bool kW = decltype(wide_c)::value;
-        for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
-          const int s = it & 1;
-          const int live = min(kTileKeys, un.key1 - key);
+      // A tile; `whole`: 128 keys that all rows of the unit see. Code of its own for each kind of unit and tile: the
+      // wide conversion in the others' loop cost them 35 us of 240 (and the softmax's part another 30).
+      auto convert = [&](const PagedUnit& un, int key, int all, auto wide_c, auto whole_c) {
+        constexpr bool kW = decltype(wide_c)::value, kWhole = decltype(whole_c)::value;
+        const int s = it & 1;
+        const int live = kWhole ? kTileKeys : min(kTileKeys, un.key1 - key);
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            mbar_wait(&raw_full[kv], it & 1, wg);
-            const uint8_t* raw = smem + TileSmem::kRaw + kv * TileSmem::kRawTile;
-            const uint8_t* scale = smem + TileSmem::kScale + kv * 128;
-            uint8_t* dst = (kv ? sV : sK) + s * T32;
-            // the tile's largest scale: lane i looks at rows 4i..4i+3; NaN rows and those behind the last key do not count
-            uint32_t top = 0u;
-            bool some_nan = false;
-            {
-              const uint32_t w = reinterpret_cast<const uint32_t*>(scale)[lane];
+        for (int kv = 0; kv < 2; ++kv) {
+          mbar_wait(&raw_full[kv], it & 1, wg);
+          const uint8_t* raw = smem + TileSmem::kRaw + kv * TileSmem::kRawTile;
+          const uint8_t* scale = smem + TileSmem::kScale + kv * 128;
+          uint8_t* dst = (kv ? sV : sK) + s * T32;
+          // the tile's largest scale: lane i looks at rows 4i..4i+3; NaN rows and those behind the last key do not count
+          uint32_t top = 0u;
+          bool some_nan = false;
+          {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(scale)[lane];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t b = (w >> (8 * i)) & 255u;
-                if (4 * lane + i < live) {
-                  if (b != 255u) top = max(top, b);
-                  some_nan |= b == 255u;
-                }
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t b = (w >> (8 * i)) & 255u;
+              if (kWhole || 4 * lane + i < live) {
+                if (b != 255u) top = max(top, b);
+                some_nan |= b == 255u;
               }
             }
-            const uint32_t ref = kW ? 127u : __reduce_max_sync(0xffffffffu, top);
-            const bool near = live == kTileKeys && !__any_sync(0xffffffffu, some_nan);
-            // Pieces 2e and 2e + 1 of a row; lanes of the second 64 dims take the odd one first, so that the eight
-            // lanes of a row hit all banks once. All of a tile is read before its place in the ring is waited for.
-            uint2 x0[8], x1[8];
-            uint32_t f[8];
-            {
-              const uint8_t* src = raw + sub * 128 + e * 16;
-              const uint32_t base = near_base(ref);
+          }
+          const uint32_t ref = kW ? 127u : __reduce_max_sync(0xffffffffu, top);
+          const bool near = !__any_sync(0xffffffffu, some_nan);
+          // all of a tile is read before its place in the ring is waited for
+          uint2 x0[8], x1[8];
+          uint32_t f[8];
+          {
+            const uint8_t* src = raw + sub * 128 + e * 16;
+            const uint32_t base = near_base(ref);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                x0[i] = *reinterpret_cast<const uint2*>(src + (odd ? 8 : 0) + i * 2048);
-                x1[i] = *reinterpret_cast<const uint2*>(src + (odd ? 0 : 8) + i * 2048);
-                f[i] = scale[16 * i + sub];
-              }
-              if constexpr (kW) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = __float_as_uint(e8m0_value(f[i]));
-              } else if (near) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = f[i] * 0x04000400u + base;
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = near_factor(f[i], ref);
-              }
-              if (live < kTileKeys) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  // what lies behind the last key must not reach the sum, whatever it is
-                  if (16 * i + sub >= live) {
-                    f[i] = 0u;
-                    x0[i] = x1[i] = make_uint2(0u, 0u);
-                  }
-                }
-              }
+            for (int i = 0; i < 8; ++i) {
+              x0[i] = *reinterpret_cast<const uint2*>(src + (odd ? 8 : 0) + i * 2048);
+              x1[i] = *reinterpret_cast<const uint2*>(src + (odd ? 0 : 8) + i * 2048);
+              f[i] = scale[16 * i + sub];
             }
-            mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((it >> 1) & 1) ^ 1u, wg);
-            if (ct == 0) refs[kv * 4 + (it & 3)] = ref | (kW && kv == 0 ? kWide : 0u);
-            uint8_t* dst0 = dst + tile_offset(sub, 2 * e + (odd ? 1 : 0));
-            uint8_t* dst1 = dst + tile_offset(sub, 2 * e + (odd ? 0 : 1));
             if constexpr (kW) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                *reinterpret_cast<uint4*>(dst0 + i * 2048) = dequant8(x0[i], __uint_as_float(f[i]));
-                *reinterpret_cast<uint4*>(dst1 + i * 2048) = dequant8(x1[i], __uint_as_float(f[i]));
-              }
+              for (int i = 0; i < 8; ++i) f[i] = __float_as_uint(e8m0_value(f[i]));
+            } else if (near) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f[i] = f[i] * 0x04000400u + base;
             } else {
 #pragma unroll
+              for (int i = 0; i < 8; ++i) f[i] = near_factor(f[i], ref);
+            }
+            if constexpr (!kWhole) {
+#pragma unroll
               for (int i = 0; i < 8; ++i) {
-                *reinterpret_cast<uint4*>(dst0 + i * 2048) = e4m3x8_f16(x0[i], f[i]);
-                *reinterpret_cast<uint4*>(dst1 + i * 2048) = e4m3x8_f16(x1[i], f[i]);
+                // what lies behind the last key must not reach the sum, whatever it is
+                if (16 * i + sub >= live) {
+                  f[i] = 0u;
+                  x0[i] = x1[i] = make_uint2(0u, 0u);
+                }
               }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(kv ? &v_full[s] : &k_full[s]);
-              mbar_arrive(&raw_empty[kv]);
+          }
+          mbar_wait(kv ? &v_empty[s] : &k_empty[s], ((it >> 1) & 1) ^ 1u, wg);
+          if (ct == 0) refs[kv * 4 + (it & 3)] = ref | (kW && kv == 0 ? kWide : 0u);
+          uint8_t* dst0 = dst + tile_offset(sub, piece0);
+          uint8_t* dst1 = dst + tile_offset(sub, piece1);
+          if constexpr (kW) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              *reinterpret_cast<uint4*>(dst0 + i * 2048) = dequant8(x0[i], __uint_as_float(f[i]));
+              *reinterpret_cast<uint4*>(dst1 + i * 2048) = dequant8(x1[i], __uint_as_float(f[i]));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              *reinterpret_cast<uint4*>(dst0 + i * 2048) = e4m3x8_f16(x0[i], f[i]);
+              *reinterpret_cast<uint4*>(dst1 + i * 2048) = e4m3x8_f16(x1[i], f[i]);
             }
           }
-          if (key > un.key0) continue;
-          // the unit's queries, in place: |q| / 2^x < 4 for the largest of a row; as they are where the unit is wide
-          const int rows = min(kTileRows, un.rows - un.row0);
-          for (int t = 0; t * 128 < rows; ++t) {
-            mbar_wait(&q_raw[t], n_unit[t] & 1, wg);
-            ++n_unit[t];
-            uint8_t* qt = sQ + t * T32;
-            if (kW) q_scale[(u & 1) * 256 + t * 128 + ct] = 127u;
-#pragma unroll 2
-            for (int i = kW ? 8 : 0; i < 8; ++i) {
-              const int r = 16 * i + sub;
-              uint4* pa = reinterpret_cast<uint4*>(qt + tile_offset(r, e));
-              uint4* pb = reinterpret_cast<uint4*>(qt + tile_offset(r, 8 + e));
-              float a[8], b[8];
-              unpack_bf16x8(*pa, a);
-              unpack_bf16x8(*pb, b);
-              float m = fmax3_nan(amax8(a), amax8(b), 0.f);
-#pragma unroll
-              for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
-              const uint32_t ex = query_exponent(m);
-              const float down = __uint_as_float((254u - ex) << 23);
-              if (e == 0) q_scale[(u & 1) * 256 + t * 128 + r] = static_cast<uint8_t>(ex);
-              *pa = make_uint4(pack_half2(a[0] * down, a[1] * down), pack_half2(a[2] * down, a[3] * down),
-                               pack_half2(a[4] * down, a[5] * down), pack_half2(a[6] * down, a[7] * down));
-              *pb = make_uint4(pack_half2(b[0] * down, b[1] * down), pack_half2(b[2] * down, b[3] * down),
-                               pack_half2(b[4] * down, b[5] * down), pack_half2(b[6] * down, b[7] * down));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[t]);
+          if (!kWhole && kv && key + live > all)  // each thread what it has just written
+            clean(dst, key, live, key - kTileKeys < un.key0 || key <= all, un.rows - un.row0, wide_c);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(kv ? &v_full[s] : &k_full[s]);
+            mbar_arrive(&raw_empty[kv]);
           }
         }
+        ++it;
+      };
+      // a unit's queries, in place: |q| / 2^x < 4 for the largest of a row; as they are where the unit is wide
+      auto convert_queries = [&](int u, const PagedUnit& un, auto wide_c) {
+        constexpr bool kW = decltype(wide_c)::value;
+        const int rows = min(kTileRows, un.rows - un.row0);
+        for (int t = 0; t * 128 < rows; ++t) {
+          mbar_wait(&q_raw[t], n_unit[t] & 1, wg);
+          ++n_unit[t];
+          uint8_t* qt = sQ + t * T32;
+          if (kW) q_scale[(u & 1) * 256 + t * 128 + ct] = 127u;
+#pragma unroll 2
+          for (int i = kW ? 8 : 0; i < 8; ++i) {
+            const int r = 16 * i + sub;
+            uint4* pa = reinterpret_cast<uint4*>(qt + tile_offset(r, e));
+            uint4* pb = reinterpret_cast<uint4*>(qt + tile_offset(r, 8 + e));
+            float a[8], b[8];
+            unpack_bf16x8(*pa, a);
+            unpack_bf16x8(*pb, b);
+            float m = fmax3_nan(amax8(a), amax8(b), 0.f);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m = fmax3_nan(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+            const uint32_t ex = query_exponent(m);
+            const float down = __uint_as_float((254u - ex) << 23);
+            if (e == 0) q_scale[(u & 1) * 256 + t * 128 + r] = static_cast<uint8_t>(ex);
+            *pa = make_uint4(pack_half2(a[0] * down, a[1] * down), pack_half2(a[2] * down, a[3] * down),
+                             pack_half2(a[4] * down, a[5] * down), pack_half2(a[6] * down, a[7] * down));
+            *pb = make_uint4(pack_half2(b[0] * down, b[1] * down), pack_half2(b[2] * down, b[3] * down),
+                             pack_half2(b[4] * down, b[5] * down), pack_half2(b[6] * down, b[7] * down));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[t]);
+        }
+      };
+      auto run_unit = [&](int u, const PagedUnit& un, auto wide_c) {
+        const int all = seen_by_all(un, p.group), whole = min(all, un.key1);
+        int key = un.key0;
+        if (key + kTileKeys <= whole)
+          convert(un, key, all, wide_c, std::true_type{});
+        else
+          convert(un, key, all, wide_c, std::false_type{});
+        convert_queries(u, un, wide_c);
+        for (key += kTileKeys; key + kTileKeys <= whole; key += kTileKeys) convert(un, key, all, wide_c, std::true_type{});
+        for (; key < un.key1; key += kTileKeys) convert(un, key, all, wide_c, std::false_type{});
       };
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
@@ -469,9 +521,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         __syncwarp();
         if (lane == 0) mbar_arrive(&wide_empty[slot]);
         if (wide)
-          convert(u, un, std::true_type{});
+          run_unit(u, un, std::true_type{});
         else
-          convert(u, un, std::false_type{});
+          run_unit(u, un, std::false_type{});
       }
     }
   } else if (warp >= 12) {
@@ -516,10 +568,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     if (warp == 14) {
       // ---------------------------------------------------------- pages; lane i takes page i of a tile
       const int ps = 1 << p.page_shift;
-      int it = 0, tails = 0;  // key tiles so far, over all units
+      int it = 0;  // key tiles so far, over all units
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
         const int* pages = p.pages + un.page0;
+        const int all = seen_by_all(un, p.group);
         for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
           const int s = it & 1;
           const uint32_t ph = (it >> 1) & 1;
@@ -542,7 +595,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               }
             }
           } else {
-            const bool tail = live < kTileKeys;
             const uint32_t bytes = static_cast<uint32_t>(n_pages * ps) * 256u;
             if (lane == 0) {
               mbar_wait(&k_empty[s], ph ^ 1u, wg);
@@ -554,7 +606,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               tma_load_2d(dst, &tp.k_map, &k_full[s], 0, row);
               tma_load_2d(dst + 16384, &tp.k_map, &k_full[s], 64, row);
             }
-            uint64_t* vb = tail ? v_raw : &v_full[s];
+            uint64_t* vb = live < kTileKeys || key + kTileKeys > all ? &v_raw[s] : &v_full[s];  // warps 8-11 clean it first
             if (lane == 0) {
               mbar_wait(&v_empty[s], ph ^ 1u, wg);
               mbar_expect_tx(vb, bytes);
@@ -564,16 +616,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               uint8_t* dst = sV + s * T32 + lane * (ps * 128);
               tma_load_2d(dst, &tp.v_map, vb, 0, row);
               tma_load_2d(dst + 16384, &tp.v_map, vb, 64, row);
-            }
-            if (tail) {
-              // what lies behind the last key must not reach the sum, whatever it is: zero values
-              mbar_wait(v_raw, tails & 1, wg);
-              ++tails;
-              for (int i = lane; i < (kTileKeys - live) * 16; i += 32)
-                *reinterpret_cast<uint4*>(sV + s * T32 + tile_offset(live + (i >> 4), i & 15)) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&v_full[s]);
             }
           }
         }
@@ -715,13 +757,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     int it = 0;  // key tiles so far, over all units
     for (int u = u_begin; u < u_end; ++u) {
       int key0, key1, limit;
-      bool active;
+      bool active, masked;
       {
         const PagedUnit un = read_unit(p.units + u);
         key0 = un.key0;
         key1 = un.key1;
         const int unit_rows = min(kTileRows, un.rows - un.row0);
         active = t * 128 < unit_rows;
+        masked = seen_by_all(un, p.group) < un.key1;
         limit = max(un.vis, un.past + (un.row0 + min(t * 128 + row, unit_rows - 1)) / p.group + 1);
       }
       if (!active) {
@@ -860,14 +903,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       const float inv = inv_l * unit_v;
       const long long orow = out_row_of(min(t * 128 + row, unit_rows - 1));
       float* slot = p.part + static_cast<long long>(un.slot0 + split) * kTileSlot;
-      float probe = 0.f;  // NaN if any sum is not finite
+      const bool some_nan = masked && *poisoned != 0u;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t r[32];
         tmem_ld32(tO + c * 32, r);
         tmem_ld_wait();
+        if (some_nan) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) probe = fmaf(__uint_as_float(r[i]), 0.f, probe);
+          for (int i = 0; i < 32; ++i)
+            if (poison[c * 32 + i] < limit) r[i] = 0x7fc00000u;
+        }
         if (live && nsplit == 1) {
           store_row32(p.o + orow * 16 + c * 4, r, inv);
         } else if (live) {
@@ -885,36 +931,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         else if (p.lse)
           p.lse[orow] = lse_of(m_run, l_run);
       }
-      // rows whose scores are fine but whose sum is not, behind keys they do not see
-      unsigned redo = __ballot_sync(0xffffffffu, live && !(probe == 0.f) && l_run < INFINITY && limit < un.key1);
-      while (redo) {
-        const int src = __ffs(redo) - 1;
-        redo &= redo - 1;
-        const int lim = __shfl_sync(0xffffffffu, limit, src);
-        const float m = finite_or_zero(__shfl_sync(0xffffffffu, m_run, src)), f = __shfl_sync(0xffffffffu, inv_l, src);
-        const int r = t * 128 + (warp & 3) * 32 + src;
-        const long long out_row = out_row_of(r);
-        const float4 acc = row_sum_seen<kE4m3>(p, p.pages + un.page0, un.head, reinterpret_cast<const uint2*>(p.q + out_row * 16),
-                                               un.key0, lim, m);
-        __syncwarp();  // the row as its thread wrote it; only what is not finite is replaced
-        if (nsplit == 1) {
-          uint2* dst = reinterpret_cast<uint2*>(p.o + out_row * 16) + lane;
-          uint2 w = *dst;
-          if ((w.x & 0x7f80u) == 0x7f80u) w.x = (w.x & 0xffff0000u) | (pack_bf162(acc.x * f, 0.f) & 0xffffu);
-          if ((w.x & 0x7f800000u) == 0x7f800000u) w.x = (w.x & 0xffffu) | (pack_bf162(0.f, acc.y * f) & 0xffff0000u);
-          if ((w.y & 0x7f80u) == 0x7f80u) w.y = (w.y & 0xffff0000u) | (pack_bf162(acc.z * f, 0.f) & 0xffffu);
-          if ((w.y & 0x7f800000u) == 0x7f800000u) w.y = (w.y & 0xffffu) | (pack_bf162(0.f, acc.w * f) & 0xffff0000u);
-          *dst = w;
-        } else {
-          float4* dst = reinterpret_cast<float4*>(slot) + lane * kTileRows + r;
-          float4 w = *dst;
-          if (!isfinite(w.x)) w.x = acc.x;
-          if (!isfinite(w.y)) w.y = acc.y;
-          if (!isfinite(w.z)) w.z = acc.z;
-          if (!isfinite(w.w)) w.w = acc.w;
-          *dst = w;
-        }
-      }
+      if (masked && lane == 0) mbar_arrive(&poison_empty[t]);  // the warp has read it: converged since the loads above
       if (nsplit > 1) {
         // the last range to arrive merges all, in the order of the ranges
         const int threads = unit_rows > 128 ? 256 : 128;

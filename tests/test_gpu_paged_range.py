@@ -208,3 +208,74 @@ def test_small_queries_beside_a_tile_of_nan_scales(cuda_ready, q_len):
     assert np.isnan(o[free:]).all() and np.isnan(lse[free:]).all()
     if free:
         check_rows(paged, pool, table, q, q_len, 256, 0, o, lse, rows=[0, 1, 40, free - 1])
+
+
+def bad_rows(pool, table, page, head, bad):
+    """Puts what is not finite into value rows of KV head `head`: {key: (dim or None for the whole row, value)}."""
+    for j, (d, x) in bad.items():
+        at = (int(table[0][j // page]), head, j % page)
+        if pool.kv_dtype == "bf16":
+            pool.v[at + ((slice(None) if d is None else d),)] = x
+        elif d is None:
+            pool.v_scale.view(torch.uint8)[at] = 255  # over a payload that is finite
+        else:
+            pool.v.view(torch.uint8)[at + (d,)] = 0x7F
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("hq,hkv,page,q_len,past,visible", [
+    (4, 4, 16, 300, 0, 0), (4, 2, 64, 200, 1000, 0), (8, 2, 128, 129, 71, 150), (6, 2, 32, 260, 5000, 5100), (4, 4, 16, 90, 38, 0),
+    (4, 2, 16, 3, 300, 0)])
+def test_values_that_are_not_finite_reach_those_that_see_them(cuda_ready, hq, hkv, page, q_len, past, visible, wide, kv):
+    # bad values in several tiles of the chunk and of what lies before it, each in a dim of its own or in a whole row:
+    # a query has NaN or infinity in exactly the dims of the bad values that it sees
+    g = torch.Generator().manual_seed(past)
+    n = past + q_len
+    k, v = (torch.randn(1, hkv, n, 128, generator=g) for _ in range(2))
+    if wide:
+        v[0, :, 0] *= 2.0 ** -20
+    paged, pool, table, batch = cached(hq, hkv, page, kv, [q_len], [n], k, v, visible=[visible])
+    q = torch.randn(q_len, hq, 128, generator=g).to(torch.bfloat16).cuda()
+    clean = pool_values(pool)
+    inf = float("inf")
+    bad = {n - 1: (None, float("nan")), past + q_len // 3: (127, inf), past + q_len // 2: (64, float("nan")),
+           past + q_len // 2 + 1: (7, -inf), past + 2 * q_len // 3: (7, inf)}
+    bad_rows(pool, table, page, hkv - 1, bad)
+    o, lse = attend(paged, pool, batch, q)
+    kk, vv = (sequence_rows(x, table, 0, n, page) for x in clean)
+    group = hq // hkv
+    for i in sorted({0, q_len // 3 - 1, q_len // 3, q_len // 2 - 1, q_len // 2, q_len // 2 + 1, 2 * q_len // 3, q_len - 2, q_len - 1}):
+        limit = max(visible, past + i + 1)
+        hit = np.zeros((hq, 128), dtype=bool)
+        for j, (d, _) in bad.items():
+            if j < limit:
+                hit[-group:, slice(None) if d is None else d] = True
+        assert np.array_equal(~np.isfinite(o[i]), hit), i
+        ref, l, absv, mag = PG.chunk_attention(as_f64(q[i:i + 1]), kk[:, :limit], vv[:, :limit], limit)
+        tol = attend_tolerance(ref, absv, mag, small_weights(kv, vv[:, :limit]))
+        assert np.all((np.abs(o[i] - ref[0]) <= tol[0]) | hit), i
+        assert np.all(np.abs(lse[i] - l[0]) <= lse_tolerance(l, mag)[0])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_value_that_is_not_finite_costs_no_time(cuda_ready, kv):
+    # whole sequences a CTA: one NaN in the last row of each, unseen by all queries but the last
+    n, hkv, length, q_len = 38, 4, 6000, 64
+    dense = [torch.randn(n, hkv, length, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    q = torch.randn(n * q_len, 16, 128, device="cuda", dtype=torch.bfloat16)
+    times = []
+    for bad in (False, True):
+        if bad:
+            dense[1][:, :, -1, 0] = float("nan")
+        paged, pool, table, batch = cached(16, hkv, 64, kv, [q_len] * n, [length] * n, *dense)
+        attend(paged, pool, batch, q)
+        a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+        a.record()
+        for _ in range(5):
+            o = paged.attend(batch, q, pool)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+        assert torch.isfinite(o.view(n, q_len, 16, 128)[:, :-1]).all()
+    assert paged.device_status() == 0 and times[1] < 2 * times[0], times
