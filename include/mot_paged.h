@@ -82,7 +82,7 @@ typedef struct {
   int32_t max_pages;     /* largest number of table entries in use           */
 } mot_paged_config;
 
-/* Norm gains, device bf16 [128]; copied at create. */
+/* Norm gains, bf16 [128] in memory of the current device; copied at create. */
 typedef struct {
   const void *q_norm, *k_norm;
 } mot_paged_weights;

@@ -244,6 +244,16 @@ bool plan_units(const std::vector<PagedTile>& tiles, int heads, int ctas, const 
   return true;
 }
 
+// device memory of the current device
+bool on_current_device(const void* p) {
+  int dev = -1;
+  cudaPointerAttributes a{};
+  if (cudaGetDevice(&dev) == cudaSuccess && cudaPointerGetAttributes(&a, p) == cudaSuccess)
+    return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == dev);
+  cudaGetLastError();
+  return false;
+}
+
 bool paged_device_ok(const mot_paged* h) {
   int dev = -1;
   return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
@@ -313,6 +323,8 @@ mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights
   if (st != MOT_OK) return st;
   if (!w || !w->q_norm || !w->k_norm) return MOT_ERR_INVALID_ARGUMENT;
   if (!aligned16(w->q_norm) || !aligned16(w->k_norm)) return MOT_ERR_ALIGNMENT;
+  // the kernels below read them: another GPU's memory would be an illegal address
+  if (!on_current_device(w->q_norm) || !on_current_device(w->k_norm)) return MOT_ERR_INVALID_ARGUMENT;
   mot_paged* h = new (std::nothrow) mot_paged();
   if (!h) return MOT_ERR_CUDA;
   h->cfg = *cfg;

@@ -27,6 +27,12 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def mot_paged_create(cfg: MotPagedConfig, weights: Dict[str, torch.Tensor], stream=None) -> c_void_p:
+    for n in ("q_norm", "k_norm"):
+        t = weights[n]
+        if t.shape != (128,):
+            raise ValueError(f"{n} must be [128] (got {list(t.shape)})")
+        if t.is_cuda and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{n} must be on the current device, {torch.cuda.current_device()} (got {t.device})")
     w = MotPagedWeights(*[_dptr(weights[n], _BF16, n) for n in ("q_norm", "k_norm")])
     h = c_void_p()
     check(lib().mot_paged_create(byref(cfg), byref(w), _stream(stream), byref(h)), "mot_paged_create")

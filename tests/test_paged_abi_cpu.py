@@ -117,6 +117,42 @@ def test_bindings_refuse_host_tensors():
         MotPagedPool(pages[..., :64], pages[..., :64])
 
 
+class FakeCudaTensor:
+    # what the binding looks at before it hands over an address
+    is_cuda, dtype = True, torch.bfloat16
+
+    def __init__(self, device, shape=(128,)):
+        self.index, self.shape, self.device = device, torch.Size(shape), f"cuda:{device}"
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_gains_elsewhere_or_of_another_size_reach_no_kernel(monkeypatch):
+    # the kernels of create read 128 values of each gain on the current device
+    from mot_flow_matching_b200 import paged as binding
+
+    def no_library():
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(binding, "lib", no_library)
+    monkeypatch.setattr(binding, "_stream", lambda s: c_void_p(0))
+    good = FakeCudaTensor(0)
+    for bad in (FakeCudaTensor(1), FakeCudaTensor(0, (64,)), FakeCudaTensor(0, (1, 128))):
+        for weights in ({"q_norm": bad, "k_norm": good}, {"q_norm": good, "k_norm": bad}, {"q_norm": bad, "k_norm": bad}):
+            with pytest.raises(ValueError, match="_norm must be"):
+                binding.MotPaged(weights)
+    with pytest.raises(AssertionError, match="library"):
+        binding.MotPaged({"q_norm": good, "k_norm": good})
+
+
 def test_bindings_refuse_lengths_and_pages_that_are_not_32_bit_integers():
     from mot_flow_matching_b200.paged import mot_paged_batch_set
     good = dict(q_len=[1, 1], kv_len=[3, 4], table=[[0], [1]], visible=[0, 0])
