@@ -110,8 +110,10 @@ class MotPagedBatch:
         self.batch = 0
         if self.paged.handle is None or not self.handle:
             raise ValueError("the batch or its handle has been closed")
+        q_len, kv_len = _host_i32(q_len, "q_len"), _host_i32(kv_len, "kv_len")
         mot_paged_batch_set(self.handle, q_len, kv_len, table, n_pages, visible, stream)
-        self.batch, self.tokens, self.kv_max = len(q_len), int(sum(q_len)), int(max(kv_len))
+        # of the 32-bit lengths: sums in the caller's type may wrap
+        self.batch, self.tokens, self.kv_max = q_len.numel(), int(q_len.sum()), int(kv_len.max())
         c = self.paged.cfg
         self.q_shape = (self.tokens, c.n_q_heads, 128)
         self.qkv_shape = (self.tokens, (c.n_q_heads + 2 * c.n_kv_heads) * 128)

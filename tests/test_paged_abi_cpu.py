@@ -165,6 +165,25 @@ def test_bindings_refuse_lengths_and_pages_that_are_not_32_bit_integers():
         mot_paged_batch_set(None, n_pages=2, **{**good, "q_len": [1.5, 1]})
 
 
+@pytest.mark.parametrize("q_len,kv_len", [([200, 100], [250, 130]), ([1, 0, 127], [1, 5, 127])])
+def test_lengths_of_any_integer_type_add_up(monkeypatch, q_len, kv_len):
+    # 200 + 100 is 44 in 8 bits
+    from mot_flow_matching_b200 import paged as binding
+    monkeypatch.setattr(binding, "mot_paged_batch_set", lambda *a, **k: None)
+    paged, batch = object.__new__(binding.MotPaged), object.__new__(binding.MotPagedBatch)
+    paged.handle, paged.cfg, batch.paged, batch.handle = None, cfg(), paged, c_void_p(16)
+    try:
+        for kind in (list, tuple, np.uint8, np.int16, np.int64, torch.uint8, torch.int16, torch.int64):
+            make = (lambda x: torch.tensor(x, dtype=kind)) if isinstance(kind, torch.dtype) else \
+                kind if kind in (list, tuple) else (lambda x: np.array(x, dtype=kind))
+            paged.handle = c_void_p(16)
+            batch.set(make(q_len), make(kv_len), [[0]], 1)
+            assert (batch.batch, batch.tokens, batch.kv_max) == (len(q_len), sum(q_len), max(kv_len)), kind
+            assert batch.q_shape == (sum(q_len), 32, 128)
+    finally:
+        paged.handle, batch.handle = None, c_void_p()  # not the library's: nothing to free
+
+
 def test_a_closed_handle_sets_no_batch():
     # the batch object's memory in the library refers to the handle's
     from mot_flow_matching_b200.paged import MotPaged, MotPagedBatch
