@@ -13,6 +13,7 @@ run in libmotattn.so.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from ctypes import byref, c_size_t, c_void_p
 from typing import Dict, Optional, Sequence
 
@@ -37,6 +38,15 @@ def mot_paged_create(cfg: MotPagedConfig, weights: Dict[str, torch.Tensor], stre
     h = c_void_p()
     check(lib().mot_paged_create(byref(cfg), byref(w), _stream(stream), byref(h)), "mot_paged_create")
     return h
+
+
+def _external(stream) -> torch.cuda.Stream:
+    return torch.cuda.ExternalStream(_stream(stream).value or 0)
+
+
+def _on_stream(stream):
+    """Memory allocated under it may be reused once work of `stream` is done (None: the current stream)."""
+    return nullcontext() if stream is None else torch.cuda.stream(_external(stream))
 
 
 def _host_i32(v, name: str) -> Optional[torch.Tensor]:
@@ -102,7 +112,7 @@ class MotPagedBatch:
         n = c_size_t(0)
         check(lib().mot_paged_query_workspace(self.handle, byref(n)), "mot_paged_query_workspace")
         self.workspace_bytes = n.value
-        self._ws = None
+        self._ws, self._ws_streams = None, set()
         self.batch = self.tokens = self.kv_max = 0
 
     def set(self, q_len: Sequence[int], kv_len: Sequence[int], table, n_pages: int,
@@ -118,9 +128,16 @@ class MotPagedBatch:
         self.q_shape = (self.tokens, c.n_q_heads, 128)
         self.qkv_shape = (self.tokens, (c.n_q_heads + 2 * c.n_kv_heads) * 128)
 
-    def workspace(self, device="cuda") -> torch.Tensor:
+    def workspace(self, device="cuda", stream=None) -> torch.Tensor:
+        """The batch's own workspace, for work on `stream` (None: the current one)."""
+        raw = self.paged._on(stream)
         if self._ws is None:
-            self._ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+            with _on_stream(stream):
+                self._ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+            self._ws_streams = {raw}
+        if raw not in self._ws_streams:
+            self._ws.record_stream(_external(raw))  # not another's memory before this stream is done with it
+            self._ws_streams.add(raw)
         return self._ws
 
     def close(self):
@@ -168,6 +185,9 @@ class MotPaged:
     def new_batch(self) -> MotPagedBatch:
         return MotPagedBatch(self)
 
+    # With `stream` the outputs and the workspace that a call allocates are that stream's: a tensor that the caller frees
+    # goes back to it. Tensors that the caller passes are the caller's to keep until the stream is done with them.
+    #
     # The calls below run once per layer and step, where a single token's kernel takes a few microseconds: the
     # checks are written to cost little (plain integers for pointers, no intermediate objects).
 
@@ -201,7 +221,8 @@ class MotPaged:
         qkv: [T, (Hq + 2 Hkv) * 128]."""
         self._check(batch, pool)
         if q is None:
-            q = torch.empty(batch.q_shape, dtype=_BF16, device=qkv.device)
+            with _on_stream(stream):
+                q = torch.empty(batch.q_shape, dtype=_BF16, device=qkv.device)
         st = self._append(self.handle, batch.handle, self._ptr(qkv, _BF16, batch.qkv_shape, "qkv"), pool.ref,
                           self._ptr(q, _BF16, batch.q_shape, "q"), self._on(stream))
         if st:
@@ -225,11 +246,13 @@ class MotPaged:
         MotAttnLayer.forward takes (rows: that of k, v when given, else the
         longest sequence's; rows behind a sequence are not written)."""
         self._check(batch, pool)
-        if k is None:
-            k = torch.empty((batch.batch, self.cfg.n_kv_heads, batch.kv_max, 128) if v is None else v.shape, dtype=_BF16,
-                            device=pool.k.device)
-        if v is None:
-            v = torch.empty_like(k)
+        if k is None or v is None:
+            with _on_stream(stream):
+                if k is None:
+                    k = torch.empty((batch.batch, self.cfg.n_kv_heads, batch.kv_max, 128) if v is None else v.shape,
+                                    dtype=_BF16, device=pool.k.device)
+                if v is None:
+                    v = torch.empty_like(k)
         rows = k.shape[2] if k.dim() == 4 else -1
         shape = (batch.batch, self.cfg.n_kv_heads, rows, 128)
         st = self._load(self.handle, batch.handle, pool.ref, self._ptr(k, _BF16, shape, "k"),
@@ -246,9 +269,10 @@ class MotPaged:
         self._check(batch, pool)
         shape = batch.q_shape
         if o is None:
-            o = torch.empty_like(q)
+            with _on_stream(stream):
+                o = torch.empty_like(q)
         if workspace is None:
-            workspace = batch.workspace(q.device)
+            workspace = batch.workspace(q.device, stream)
         st = self._attend(self.handle, batch.handle, self._ptr(q, _BF16, shape, "q"), pool.ref,
                           self._ptr(o, _BF16, shape, "o"),
                           None if lse is None else self._ptr(lse, _F32, shape[:2], "lse"),

@@ -1,5 +1,5 @@
 """Calls of the paged prefix-KV cache (include/mot_paged.h) around the kernels:
-addresses that are no device memory of the current device."""
+addresses that are no device memory of the current device, the `stream` argument."""
 from ctypes import byref, c_void_p
 
 import pytest
@@ -7,6 +7,7 @@ import torch
 
 from mot_flow_matching_b200 import _abi
 from tests.gpu_helpers import ensure_built
+from tests.test_gpu_paged import fill_pool, make_paged, make_table, write_sequences
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +27,57 @@ def test_create_refuses_gains_in_host_memory(cuda_ready):
     out = c_void_p()
     assert _abi.lib().mot_paged_create(byref(cfg), byref(w), None, byref(out)) == _abi.MOT_OK
     _abi.lib().mot_paged_destroy(out)
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_outputs_allocated_for_a_stream_are_that_streams(cuda_ready, as_int):
+    # Memory that the current stream has freed but not yet finished writing must not become an output of work on
+    # another stream: the current stream sleeps, then fills tensors of the outputs' sizes, which are freed at once.
+    q_len, kv_len = [40, 1], [300, 500]
+    paged, _ = make_paged(8, 2, 16, "bf16", q_len, kv_len)
+    table, n_pages = make_table(kv_len, 16)
+    pool = fill_pool(paged, n_pages, 0)
+    write_sequences(paged, pool, table, kv_len, 1)
+    batch = paged.new_batch()
+    batch.set(q_len, kv_len, table, n_pages)
+    qkv = torch.randn(41, 12 * 128).to(torch.bfloat16).cuda()
+    q = paged.append(batch, qkv, pool)
+    o, (k, v) = paged.attend(batch, q, pool), paged.load(batch, pool)
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if as_int else side
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    for like in (q, o, k, v):
+        torch.empty_like(like).fill_(7.0)
+    # and a workspace
+    torch.empty(batch.workspace_bytes, dtype=torch.uint8, device="cuda").fill_(255)
+    b2 = paged.new_batch()
+    b2.set(q_len, kv_len, table, n_pages, stream=s)
+    q2 = paged.append(b2, qkv, pool, stream=s)
+    o2 = paged.attend(b2, q2, pool, stream=s)
+    k2, v2 = paged.load(b2, pool, stream=s)
+    torch.cuda.synchronize()
+    for a, b, rows in ((q, q2, None), (o, o2, None), (k, k2, kv_len), (v, v2, kv_len)):
+        for i in range(len(kv_len) if rows else 1):
+            x, y = (a[i, :, :rows[i]], b[i, :, :rows[i]]) if rows else (a, b)
+            assert torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+
+
+def test_a_workspace_is_kept_for_every_stream_that_uses_it(cuda_ready):
+    q_len, kv_len = [1], [5000]
+    paged, _ = make_paged(8, 2, 16, "bf16", q_len, kv_len)
+    table, n_pages = make_table(kv_len, 16)
+    pool = fill_pool(paged, n_pages, 0)
+    write_sequences(paged, pool, table, kv_len, 1)
+    q = torch.randn(1, 8, 128, device="cuda", dtype=torch.bfloat16)
+    batch, side = paged.new_batch(), torch.cuda.Stream()
+    batch.set(q_len, kv_len, table, n_pages)
+    paged.attend(batch, q, pool)
+    at, n = batch.workspace().data_ptr(), batch.workspace_bytes
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    paged.attend(batch, q, pool, stream=side)
+    batch._ws = None  # as when the batch goes, but without the wait of its cudaFree
+    assert torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr() != at  # the side stream is not done with it
+    torch.cuda.synchronize()
