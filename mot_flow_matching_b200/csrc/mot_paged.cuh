@@ -113,6 +113,12 @@ struct mot_paged_batch {
 
 namespace {
 
+// a CUDA call has failed: its error must not be taken for that of a later call
+mot_status cuda_failed() {
+  cudaGetLastError();
+  return MOT_ERR_CUDA;
+}
+
 int log2_of(int v) {
   int s = 0;
   while ((1 << s) < v) ++s;
@@ -309,7 +315,7 @@ mot_status paged_copy(mot_paged_t h, mot_paged_batch_t bt, void* k, void* v, int
   const bool e4m3 = c.kv_dtype == MOT_PAGED_E4M3;
   auto kern = e4m3 ? (store ? paged_copy_kernel<true, true> : paged_copy_kernel<true, false>)
                    : (store ? paged_copy_kernel<false, true> : paged_copy_kernel<false, false>);
-  return launch_pdl(kern, dim3(grid), dim3(256), 0, st, p) == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+  return launch_pdl(kern, dim3(grid), dim3(256), 0, st, p) == cudaSuccess ? MOT_OK : cuda_failed();
 }
 
 }  // namespace
@@ -329,6 +335,7 @@ mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights
   if (!h) return MOT_ERR_CUDA;
   h->cfg = *cfg;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaGetLastError();  // asked for below: not an earlier call's
   const bool e4m3 = cfg->kv_dtype == MOT_PAGED_E4M3;
   set_smem_attr(e4m3 ? paged_attn_tile_kernel<true> : paged_attn_tile_kernel<false>, TileSmem::bytes(e4m3));
   const uint32_t small_smem = e4m3 ? SmallShape<true>::kBytes : SmallShape<false>::kBytes;
@@ -355,7 +362,7 @@ mot_status mot_paged_create(const mot_paged_config* cfg, const mot_paged_weights
   }
   if (!ok) {
     release_paged(h);
-    return MOT_ERR_CUDA;
+    return cuda_failed();
   }
   *out = h;
   return MOT_OK;
@@ -380,7 +387,7 @@ mot_status mot_paged_batch_create(mot_paged_t h, mot_paged_batch_t* out) {
   ok = ok && cudaMalloc(&bt->dev, bt->t.words * sizeof(int)) == cudaSuccess;
   if (!ok) {
     delete bt;
-    return MOT_ERR_CUDA;
+    return cuda_failed();
   }
   *out = bt;
   return MOT_OK;
@@ -533,7 +540,7 @@ mot_status mot_paged_batch_set(mot_paged_batch_t bt, int32_t batch, const int32_
   for (const auto& pc : pieces)
     if (pc[1] > 0 && cudaMemcpyAsync(bt->dev + pc[0], bt->host.data() + pc[0], pc[1] * sizeof(int), cudaMemcpyHostToDevice,
                                      st) != cudaSuccess)
-      return MOT_ERR_CUDA;
+      return cuda_failed();
   bt->batch = batch;
   bt->tokens = static_cast<int>(tokens);
   bt->entries = static_cast<int>(entries);
@@ -587,7 +594,7 @@ mot_status mot_paged_append(mot_paged_t h, mot_paged_batch_t bt, const void* qkv
               : mode == 1 ? (e4m3 ? paged_append_kernel<true, 4, false> : paged_append_kernel<false, 4, false>)
                           : (e4m3 ? paged_append_kernel<true, 4, true> : paged_append_kernel<false, 4, true>);
   return launch_pdl(kern, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? MOT_OK
-                                                                                                          : MOT_ERR_CUDA;
+                                                                                                          : cuda_failed();
 }
 
 mot_status mot_paged_store(mot_paged_t h, mot_paged_batch_t bt, const void* k, const void* v, int32_t rows,
@@ -662,7 +669,7 @@ mot_status mot_paged_attend(mot_paged_t h, mot_paged_batch_t bt, const void* q, 
                      dim3(kTileThreads), TileSmem::bytes(e4m3), st, tp);
     }
   }
-  return e == cudaSuccess ? MOT_OK : MOT_ERR_CUDA;
+  return e == cudaSuccess ? MOT_OK : cuda_failed();
 }
 
 mot_status mot_dev_paged_plan(int32_t kind, const int32_t* tiles, int32_t n_tiles, int32_t heads, int32_t ctas,
@@ -683,9 +690,9 @@ mot_status mot_dev_paged_plan(int32_t kind, const int32_t* tiles, int32_t n_tile
 mot_status mot_paged_get_device_status(mot_paged_t h, void* stream) {
   if (!h) return MOT_ERR_INVALID_ARGUMENT;
   int v = 0;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOT_ERR_CUDA;
-  if (cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return MOT_ERR_CUDA;
-  if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess) return MOT_ERR_CUDA;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
+  if (cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return cuda_failed();
+  if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess) return cuda_failed();
   return (v & DEV_ERR_TIMEOUT) ? MOT_ERR_TIMEOUT : MOT_OK;
 }
 

@@ -1,12 +1,13 @@
 """Calls of the paged prefix-KV cache (include/mot_paged.h) around the kernels:
-addresses that are no device memory of the current device, the `stream` argument."""
+addresses that are no device memory of the current device, the `stream` argument, what a failed call leaves behind."""
 from ctypes import byref, c_void_p
 
 import pytest
 import torch
 
-from mot_flow_matching_b200 import _abi
-from tests.gpu_helpers import ensure_built
+from mot_flow_matching_b200 import _abi, synth
+from mot_flow_matching_b200.paged import MotPaged
+from tests.gpu_helpers import ensure_built, make_layer, run_forward, to_dev
 from tests.test_gpu_paged import fill_pool, make_paged, make_table, write_sequences
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +82,23 @@ def test_a_workspace_is_kept_for_every_stream_that_uses_it(cuda_ready):
     batch._ws = None  # as when the batch goes, but without the wait of its cudaFree
     assert torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr() != at  # the side stream is not done with it
     torch.cuda.synchronize()
+
+
+def test_a_failed_create_leaves_no_error_behind(cuda_ready):
+    # no room for the RoPE table of 2^22 positions (2 GiB); the next create, and the other handles', find no error of it
+    gains = {n: torch.ones(128, dtype=torch.bfloat16, device="cuda") for n in ("q_norm", "k_norm")}
+    torch.cuda.empty_cache()
+    held = torch.empty(torch.cuda.mem_get_info()[0] - (1 << 30), dtype=torch.uint8, device="cuda")
+    try:
+        with pytest.raises(_abi.MotError) as e:
+            MotPaged(gains, max_positions=1 << 22)
+        assert e.value.status == _abi.MOT_ERR_CUDA
+        wl = synth.Workload("gen", 1, 64, 0, 0, 0.0, dims=synth.LayerDims(hidden=512, n_q_heads=4, n_kv_heads=2))
+        td = to_dev(synth.make_inputs(wl, 8300, with_dy=False))
+        layer = make_layer(wl, td)
+        assert run_forward(layer, td)[3] == 0
+        layer.close()
+        MotPaged(gains, max_positions=64).close()
+    finally:
+        del held
+        torch.cuda.empty_cache()
