@@ -47,8 +47,9 @@
 // and slower: a quarter of the exponentials by polynomial (image 564 against 555
 // us, a mixed e4m3 batch 289 against 269), a second MMA warp (image 565 against
 // 552), e4m3 conversion on eight warps with fewer registers for the softmax (the
-// mixed batch 272 against 251; 251 now, 239 before wide units, large scores and
-// values that are not finite were dealt with in it).
+// mixed batch 272 against 251; 254 now, 239 before wide units, large scores and
+// values that are not finite were dealt with in it; one chunk of 64 tokens over 4500
+// keys 39.7 in place of 37).
 #pragma once
 
 #include "paged.cuh"
@@ -229,26 +230,37 @@ __device__ __forceinline__ int seen_by_all(const PagedUnit& un, int group) {
   return max(un.vis, un.past + un.row0 / group + 1);
 }
 
-// Eight values (16 bits each) of one key, dims d..: zero times an infinity or NaN
-// would reach the rows that do not see the key, so what is not finite becomes zero,
-// and its key is remembered per dim; rows that see it get NaN at the end.
+// The values of a ring tile that some rows of the unit do not see: zero times an
+// infinity or NaN would reach those rows, so what is not finite becomes zero, and
+// its key is remembered per dim; rows that see it get NaN at the end. A thread
+// takes pieces piece0 and piece1 (eight dims each) of rows sub, sub + 16, ... below
+// `live`, the first of which is key `key`. The code is kept small: it runs once or
+// twice a unit, from a cold instruction cache (unrolled it took 4 us a tile).
 template <bool kBf16>
-__device__ __forceinline__ void clean8(uint4* at, int key, int d, int* poison, volatile uint32_t* poisoned) {
+__device__ __forceinline__ void clean_tile(uint8_t* tile, int key, int live, int sub, int piece0, int piece1, int* poison,
+                                           volatile uint32_t* poisoned) {
   constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
-  uint4 v = *at;
-  const uint32_t all_ones = (((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne)) & 0x80008000u;
-  if (all_ones == 0u) return;
-  *poisoned = 1u;
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int sh = 16 * (i & 1);
-    if ((((w[i >> 1] & kExp) + kOne) >> sh) & 0x8000u) {
-      atomicMin(poison + d + i, key);
-      w[i >> 1] &= ~(0xffffu << sh);
-    }
+  auto all_ones = [](uint32_t w) { return ((w & kExp) + kOne) & 0x80008000u; };  // exponents, either half
+  uint32_t some = 0u;
+#pragma unroll 2
+  for (int r = sub; r < live; r += 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + tile_offset(r, piece0));
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + tile_offset(r, piece1));
+    some |= all_ones(v.x) | all_ones(v.y) | all_ones(v.z) | all_ones(v.w) | all_ones(w.x) | all_ones(w.y) | all_ones(w.z) | all_ones(w.w);
   }
-  *at = make_uint4(w[0], w[1], w[2], w[3]);
+  if (some == 0u) return;
+  *poisoned = 1u;
+#pragma unroll 1
+  for (int r = sub; r < live; r += 16)
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const int piece = i < 8 ? piece0 : piece1;
+      uint16_t* at = reinterpret_cast<uint16_t*>(tile + tile_offset(r, piece)) + (i & 7);
+      if ((*at & kExp & 0xffffu) == (kExp & 0xffffu)) {
+        atomicMin(poison + 8 * piece + (i & 7), key + r);
+        *at = 0;
+      }
+    }
 }
 
 template <bool kE4m3>
@@ -343,13 +355,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         if (ct == 0) *poisoned = 0u;
         named_bar_sync(2, 128);
       }
-#pragma unroll 4
-      for (int i = 0; i < 8; ++i) {
-        const int r = 16 * i + sub;
-        if (r >= live) break;
-        clean8<decltype(bf16_c)::value>(reinterpret_cast<uint4*>(tile + tile_offset(r, piece0)), key + r, 8 * piece0, poison, poisoned);
-        clean8<decltype(bf16_c)::value>(reinterpret_cast<uint4*>(tile + tile_offset(r, piece1)), key + r, 8 * piece1, poison, poisoned);
-      }
+      clean_tile<decltype(bf16_c)::value>(tile, key, live, sub, piece0, piece1, poison, poisoned);
     };
     if constexpr (!kE4m3) {
       // ---------------------------------------------------------- values on their way to the MMAs that some row must not meet
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
           mbar_wait(&v_raw[s], n_raw[s] & 1, wg);
           ++n_raw[s];
           uint8_t* tile = sV + s * T32;
-          if (key + live > all) clean(tile, key, live, key - kTileKeys < un.key0 || key <= all, un.rows - un.row0, std::true_type{});
+          if (key + live > all) clean(tile, key, live, key == un.key0 || key <= all, un.rows - un.row0, std::true_type{});
           // what lies behind the last key must not reach the sum, whatever it is: zero
           for (int r = sub; r < kTileKeys; r += 16)
             if (r >= live) {
@@ -380,12 +386,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       volatile uint32_t* refs = reinterpret_cast<volatile uint32_t*>(smem + TileSmem::kRef);
       uint8_t* q_scale = smem + TileSmem::kQScale;
       int it = 0, n_unit[2] = {0, 0};
-      // A tile; `whole`: 128 keys that all rows of the unit see. Code of its own for each kind of unit and tile: the
-      // wide conversion in the others' loop cost them 35 us of 240 (and the softmax's part another 30).
-      auto convert = [&](const PagedUnit& un, int key, int all, auto wide_c, auto whole_c) {
-        constexpr bool kW = decltype(wide_c)::value, kWhole = decltype(whole_c)::value;
+      // A tile; `masked`: its values are still to be cleaned. Code of its own for wide units: in the others' loop it cost
+      // them 35 us of 240 (and the softmax's part another 30).
+      auto convert = [&](int live, bool masked, auto wide_c) {
+        constexpr bool kW = decltype(wide_c)::value;
         const int s = it & 1;
-        const int live = kWhole ? kTileKeys : min(kTileKeys, un.key1 - key);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           mbar_wait(&raw_full[kv], it & 1, wg);
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t b = (w >> (8 * i)) & 255u;
-              if (kWhole || 4 * lane + i < live) {
+              if (4 * lane + i < live) {
                 if (b != 255u) top = max(top, b);
                 some_nan |= b == 255u;
               }
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
 #pragma unroll
               for (int i = 0; i < 8; ++i) f[i] = near_factor(f[i], ref);
             }
-            if constexpr (!kWhole) {
+            if (live < kTileKeys) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 // what lies behind the last key must not reach the sum, whatever it is
@@ -458,16 +463,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
               *reinterpret_cast<uint4*>(dst1 + i * 2048) = e4m3x8_f16(x1[i], f[i]);
             }
           }
-          if (!kWhole && kv && key + live > all)  // each thread what it has just written
-            clean(dst, key, live, key - kTileKeys < un.key0 || key <= all, un.rows - un.row0, wide_c);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(kv ? &v_full[s] : &k_full[s]);
+            if (!kv || !masked) mbar_arrive(kv ? &v_full[s] : &k_full[s]);
             mbar_arrive(&raw_empty[kv]);
           }
         }
-        ++it;
       };
       // a unit's queries, in place: |q| / 2^x < 4 for the largest of a row; as they are where the unit is wide
       auto convert_queries = [&](int u, const PagedUnit& un, auto wide_c) {
@@ -503,15 +505,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
         }
       };
       auto run_unit = [&](int u, const PagedUnit& un, auto wide_c) {
-        const int all = seen_by_all(un, p.group), whole = min(all, un.key1);
-        int key = un.key0;
-        if (key + kTileKeys <= whole)
-          convert(un, key, all, wide_c, std::true_type{});
-        else
-          convert(un, key, all, wide_c, std::false_type{});
-        convert_queries(u, un, wide_c);
-        for (key += kTileKeys; key + kTileKeys <= whole; key += kTileKeys) convert(un, key, all, wide_c, std::true_type{});
-        for (; key < un.key1; key += kTileKeys) convert(un, key, all, wide_c, std::false_type{});
+        const int all = seen_by_all(un, p.group);
+        for (int key = un.key0; key < un.key1; key += kTileKeys, ++it) {
+          const int live = min(kTileKeys, un.key1 - key);
+          const bool masked = key + live > all;
+          convert(live, masked, wide_c);
+          if (masked) {
+            // each thread what it has just written
+            clean(sV + (it & 1) * T32, key, live, key == un.key0 || key <= all, un.rows - un.row0, wide_c);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_full[it & 1]);
+          }
+          if (key == un.key0) convert_queries(u, un, wide_c);
+        }
       };
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
