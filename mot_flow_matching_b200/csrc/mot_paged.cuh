@@ -42,7 +42,9 @@ static_assert(TileSmem::bytes(true) <= 232448, "shared memory");
 // captured call keeps its launches. Measured, us of the few-rows | the 256-row
 // kernel at 16 / 24 / 32 rows: bf16, 1 sequence of 4000 keys 12.5 / 14 / 15 | 24,
 // 8 of 2000 24 / 31 / 34 | 24, 64 of 2000 165 / 204 / 312 | 105; e4m3 11.6 / 12.8 /
-// 13.5 | 28, 20.5 / 27 / 30 | 32, 105 / 153 / 196 | 157.
+// 13.5 | 28, 20.5 / 27 / 30 | 32, 105 / 153 / 196 | 157. Not followed at 25 to 32 rows of
+// one or two bf16 sequences, where the few-rows kernel would be the faster one over
+// long caches (15 against 20 to 24 us; the same at 500 keys).
 constexpr int kSmallMaxRows = 32;
 int small_rows(bool e4m3, long long mid) {
   return e4m3 ? (mid <= 64 ? 32 : 24) : mid <= 16 ? 24 : mid <= 64 ? 16 : 8;
@@ -132,16 +134,18 @@ int log2_of(int v) {
 // multiple of `granule` keys, and its ranges are merged on the device. The
 // cheaper by this count of work, in granules: a unit's prologue and epilogue cost
 // `unit`, a range of a split tile `split` more (its partial result and the
-// merge), and a share is at least `min_share`, one more where tiles have more than
-// 24 granules (a single sequence would be cut into too many ranges). Measured. Few
-// rows: 400 keys of one sequence 6.5 us in ranges of 128 keys against 8.0 in 256,
-// 4496 keys 9.8 against 9.4; 64 sequences of 1000 keys 32 us (e4m3) with these
-// costs, 37.5 with a unit at 1 and a split at 0. 256 rows: 2 us a key tile, 3 us
-// a unit, 4-5 us more a range.
+// merge), and a share is at least `min_share`, one more where a tile has more than
+// `many` granules. Measured. Costs: 64 sequences of 1000 8-bit keys, few rows, 32 us,
+// 37.5 with a unit at 1 and a split at 0; 256 rows: 2 us a key tile, 3 us a unit, 4-5
+// us more a range. min_share | one more, us in a graph, one sequence of 1000 / 2000 /
+// 3000 / 4500 keys: few rows bf16 7.2 / 7.7 / 8.0 / 9.7 | 9.1 / 8.9 / 9.1 / 9.7, e4m3
+// 7.1 / 7.9 / 8.7 / 10.6 | 7.9 / 8.2 / 9.2 / 9.8; 64 tokens of 4 heads a group bf16
+// 19.7 / 22.2 / 25.4 / 28.1 | 21.1 / 23.7 / 24.5 / 27.4, e4m3 32.4 / 34.8 / 38.7 / 44.9 |
+// 33.4 / 35.8 / 37.2 / 41.9; no difference from 8000 keys or 8 sequences on.
 struct CutRule {
-  int granule, unit, split, min_share;
+  int granule, unit, split, min_share, many;
 };
-constexpr CutRule kCutRules[2] = {{128, 2, 2, 5}, {kTileKeys, 2, 2, 7}};
+constexpr CutRule kCutRules[2] = {{128, 2, 2, 5, 30}, {kTileKeys, 2, 2, 7, 20}};
 
 struct PagedTile {
   int seq, row0, keys;
@@ -211,7 +215,7 @@ bool plan_units(const std::vector<PagedTile>& tiles, int heads, int ctas, const 
     longest = std::max(longest, granules_of(tl, rule));
   }
   // smallest share that fits
-  long long lo = std::max<long long>(rule.min_share + (longest > 24), (total + ctas - 1) / ctas), hi = lo;
+  long long lo = std::max<long long>(rule.min_share + (longest > rule.many), (total + ctas - 1) / ctas), hi = lo;
   while (!cut_units(tiles, heads, ctas, hi, rule, nullptr, 0, nullptr, nullptr)) {
     lo = hi + 1;
     hi *= 2;
