@@ -692,7 +692,7 @@ mot_status mot_dev_paged_plan(int32_t kind, const int32_t* tiles, int32_t n_tile
 }
 
 mot_status mot_paged_get_device_status(mot_paged_t h, void* stream) {
-  if (!h) return MOT_ERR_INVALID_ARGUMENT;
+  if (!h || !paged_device_ok(h)) return MOT_ERR_INVALID_ARGUMENT;
   int v = 0;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return cuda_failed();
   if (cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return cuda_failed();
