@@ -102,3 +102,22 @@ def test_a_failed_create_leaves_no_error_behind(cuda_ready):
     finally:
         del held
         torch.cuda.empty_cache()
+
+
+def test_a_workspace_from_another_stream_serves_the_default_one(cuda_ready):
+    q_len, kv_len = [1], [5000]
+    paged, _ = make_paged(8, 2, 16, "bf16", q_len, kv_len)
+    table, n_pages = make_table(kv_len, 16)
+    pool = fill_pool(paged, n_pages, 0)
+    write_sequences(paged, pool, table, kv_len, 1)
+    q = torch.randn(1, 8, 128, device="cuda", dtype=torch.bfloat16)
+    batch, side = paged.new_batch(), torch.cuda.Stream()
+    batch.set(q_len, kv_len, table, n_pages)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        o = paged.attend(batch, q, pool)
+    side.synchronize()
+    for stream in (None, 0, torch.cuda.default_stream(), side):
+        o2 = paged.attend(batch, q, pool, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16))
