@@ -145,9 +145,10 @@ struct PagedAppendParams {
 // serve all its heads; a warp has four heads at a time, and the loads of kQuads
 // such fours are issued before the first is used. kWhole: a warp takes a whole
 // token, the next fours on their way; else a token is cut into strips of kQuads.
-// Bound by bytes, and by a warp's chain of loads and norms where tokens are few:
-// 2 x 4096 tokens of 32/8 heads into e4m3 41 us, 4.5 TB/s; one token 1.8 us in a
-// graph, 4.0 us called from Python.
+// Few tokens: a warp's chain of loads and norms. Many: no unit is full (bytes 4.5 of
+// 6.6 TB/s, issue 54%); two sets of four heads in 128 registers leave 16 warps an SM.
+// 2 x 4096 tokens of 32/8 heads into e4m3 41 us, 4.5 TB/s, into bf16 42 us, 4.75; one
+// token 1.8 us in a graph, 4.0 us called from Python.
 template <bool kE4m3, int kQuads, bool kWhole>
 __global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   grid_dep_launch();
@@ -305,8 +306,8 @@ struct PagedCopyParams {
 // all of a lane's loads are issued before the first is used. Eight lanes share
 // a row, 16 values each (32 bytes of bf16, 16 of e4m3), four rows at a time.
 // kStore: dense -> pages; otherwise pages -> dense. Bound by bytes: 56 prompts of
-// 300 to 500 tokens into e4m3 24 us (5.7 TB/s), three e4m3 sequences of about 4450
-// back 14.4 us (5.7, part of it from L2).
+// 300 to 500 tokens into e4m3 24 us (5.7 TB/s), into bf16 28.6 (6.3), three e4m3
+// sequences of about 4450 back 14.4 us (5.7, part of it from L2).
 template <bool kE4m3, bool kStore>
 __global__ void __launch_bounds__(256) paged_copy_kernel(const __grid_constant__ PagedCopyParams p) {
   grid_dep_launch();
@@ -577,10 +578,11 @@ struct Unseen {
 // The batch's tables are written by copies, never by a kernel, so they are read
 // before the grid this one depends on has completed.
 // Measured, one B200: 64 single tokens over ragged e4m3 caches of 0.4 to 8.6
-// thousand keys (554 MB) 109 us, 5.1 TB/s. Under ncu the kernel takes 112 us, its
-// loads without the arithmetic 96; a plain read of as many bytes takes 78 us. A
-// single token over 4496 bf16 keys 9.6 us, of which the keys' bytes are 2.8: the
-// rest is launch, dependent loads, and the merge of 18 ranges.
+// thousand keys (554 MB) 112 us, 4.9 TB/s (109 with one reference for all rows); the
+// same in bf16 168 us, 6.5 TB/s. Under ncu the 8-bit kernel takes 115 us, its loads
+// without the arithmetic 96; a plain read of as many bytes takes 78 us. A single
+// token over 4496 bf16 keys 9.7 us, of which the keys' bytes are 2.8: the rest is
+// launch, dependent loads, and the merge of 18 ranges.
 template <bool kE4m3>
 __global__ void __launch_bounds__(SmallShape<kE4m3>::kThreads, 2)
 paged_attn_small_kernel(const __grid_constant__ PagedSmallParams sp) {

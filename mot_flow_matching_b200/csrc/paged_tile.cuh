@@ -41,15 +41,16 @@
 // the kernel a query tile's chain S -> softmax -> P V -> next S takes about 3000:
 // 950 waiting for S, 170 to read it, 200 for the max, 1500 for exponentials and P
 // (1024 of the MUFU). Two query tiles overlap but do not hide it, and TMEM has no
-// room for a third. 2 x 4096 image tokens over 4496 keys (603 GFLOP): 547 us back
-// to back (1.10 PFLOP/s), the first launches after a pause 475 us (1.27). Prompt
-// chunks of 129 to 512 tokens, bf16: 74 us. Tried against the kernel of the time
-// and slower: a quarter of the exponentials by polynomial (image 564 against 555
-// us, a mixed e4m3 batch 289 against 269), a second MMA warp (image 565 against
-// 552), e4m3 conversion on eight warps with fewer registers for the softmax (the
-// mixed batch 272 against 251; 254 now, 239 before wide units, large scores and
-// values that are not finite were dealt with in it; one chunk of 64 tokens over 4500
-// keys 39.7 in place of 37).
+// room for a third. 2 x 4096 image tokens over 4496 keys (603 GFLOP): 554 us back
+// to back (1.09 PFLOP/s). Prompt chunks of 129 to 512 tokens, bf16: 75 us. A mixed
+// e4m3 batch 256 us, 321 when every unit is wide; one chunk of 64 tokens over 64 e4m3
+// keys 14 us, over 4500 40 us. Of these the care for wide units, large scores and
+// values that are not finite costs 1% (image), 1% (chunks), 7%, 2 and 3 us; the scan of
+// a unit's scales alone 1.2 us a call. Spills, -Xptxas -v: 8 bytes stored (bf16), 148
+// (e4m3). Tried against the kernel of the time and slower: a quarter of the
+// exponentials by polynomial (image 564 against 555 us, a mixed e4m3 batch 289 against
+// 269), a second MMA warp (image 565 against 552), e4m3 conversion on eight warps with
+// fewer registers for the softmax (the mixed batch 272 against 251).
 #pragma once
 
 #include "paged.cuh"
