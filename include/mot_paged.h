@@ -171,8 +171,8 @@ mot_status mot_paged_load(mot_paged_t h, mot_paged_batch_t bt, const mot_paged_p
  *   workspace  device, workspace_bytes from mot_paged_query_workspace
  * Rows of a page behind kv_len are never used, whatever they hold. An infinity
  * or NaN among the cached rows reaches the outputs of the queries that see it
- * (as NaN or infinity), and of no others; a finite row that a query does not see
- * has no influence on it, whatever its size.
+ * (as NaN or infinity), and of no others; a finite row that a query does not see,
+ * whatever its size, changes at most which of the roundings below its weights take.
  *
  * Scores, statistics and sums are f32 and a result does not depend on timing (fixed
  * order of every sum). In fewer bits, each rounding relative to what is rounded:
