@@ -147,13 +147,45 @@ struct ScaleSpan {
       low = __vminu2(low, __vminu2(a, b));
     }
   }
-  // over the warp: whether the largest is more than `most`, or more than `span` above the smallest
-  __device__ __forceinline__ bool beyond(int span, int most) const {
-    const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16))) - 1;
-    const int l = static_cast<int>(__reduce_min_sync(0xffffffffu, min(low & 0xffffu, low >> 16)));
-    return t > most || t - l > span;
-  }
+  // over the warp: largest plus 1 (0: none), smallest
+  __device__ __forceinline__ uint32_t largest() const { return __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)); }
+  __device__ __forceinline__ uint32_t smallest() const { return __reduce_min_sync(0xffffffffu, min(low & 0xffffu, low >> 16)); }
 };
+
+// whether a unit is wide, from the largest (plus 1, 0: none) and smallest scale bytes
+__device__ __forceinline__ bool is_wide(uint32_t k_top, uint32_t k_low, uint32_t v_top, uint32_t v_low) {
+  return static_cast<int>(k_top) - 1 > kKeyTop || static_cast<int>(k_top - 1u - k_low) > kKeySpan ||
+         static_cast<int>(v_top - 1u - v_low) > kValueSpan;
+}
+
+// a unit's scales, pieces of 16 rows from the unit's `first` on, every `stride`-th
+__device__ __forceinline__ void scan_scales(const PagedAttnParams& p, const PagedUnit& un, int first, int stride, ScaleSpan& keys,
+                                            ScaleSpan& values) {
+  const int ps16 = p.page_shift - 4;
+  const int* pages = p.pages + un.page0;
+  constexpr int kAhead = 4;  // pieces of a lane on their way
+#pragma unroll 1
+  for (int c0 = (un.key0 >> 4) + first; c0 * 16 < un.key1; c0 += stride * kAhead) {
+    uint4 k[kAhead], v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int c = c0 + stride * i;
+      if (c * 16 < un.key1) {
+        const int row = ((pages[c >> ps16] * p.Hkv + un.head) << p.page_shift) + ((c & ((1 << ps16) - 1)) << 4);
+        k[i] = *reinterpret_cast<const uint4*>(p.pool.ks + row);
+        v[i] = *reinterpret_cast<const uint4*>(p.pool.vs + row);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int rem = un.key1 - (c0 + stride * i) * 16;
+      if (rem > 0) {
+        keys.take(k[i], rem);
+        values.take(v[i], rem);
+      }
+    }
+  }
+}
 
 // f16 pair of 2^(b - ref) (b at most kKeySpan below ref, or 255: NaN); b * 0x04000400 +
 // near_base(ref) is the same where b is not 255.
@@ -295,6 +327,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
   volatile uint32_t* last_flag = tmem_slot + 2;
   volatile uint32_t* wide_flag = tmem_slot + 3;  // [2] units (e4m3)
   volatile uint32_t* poisoned = tmem_slot + 5;   // some value of the unit was taken out
+  volatile uint32_t* span = tmem_slot + 6;       // the first unit's scales: keys largest, smallest, values (e4m3)
   int* poison = reinterpret_cast<int*>(smem + TileSmem::kPoison);
 
   const int warp = warp_id(), lane = lane_id();
@@ -322,6 +355,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       mbar_init(&poison_empty[i], 4);
     }
     *abort_flag = 0u;
+    span[0] = span[2] = 0u;
+    span[1] = span[3] = 255u;
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -523,11 +558,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
       };
       for (int u = u_begin; u < u_end; ++u) {
         const PagedUnit un = p.units[u];
-        const int slot = (u - u_begin) & 1;
-        mbar_wait(&wide_full[slot], ((u - u_begin) >> 1) & 1, wg);
-        const bool wide = wide_flag[slot] != 0u;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wide_empty[slot]);
+        bool wide;
+        if (u == u_begin) {
+          // the first unit's scales by all four warps: nothing can start before
+          ScaleSpan keys, values;
+          scan_scales(p, un, ct, 128, keys, values);
+          const uint32_t k_top = keys.largest(), k_low = keys.smallest(), v_top = values.largest(), v_low = values.smallest();
+          if (lane == 0) {
+            uint32_t* sp = const_cast<uint32_t*>(span);
+            atomicMax(sp + 0, k_top);
+            atomicMin(sp + 1, k_low);
+            atomicMax(sp + 2, v_top);
+            atomicMin(sp + 3, v_low);
+          }
+          named_bar_sync(2, 128);
+          wide = is_wide(span[0], span[1], span[2], span[3]);
+        } else {
+          const int n = u - u_begin - 1, slot = n & 1;
+          mbar_wait(&wide_full[slot], (n >> 1) & 1, wg);
+          wide = wide_flag[slot] != 0u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&wide_empty[slot]);
+        }
         if (wide)
           run_unit(u, un, std::true_type{});
         else
@@ -631,38 +683,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_attn_tile_kernel(const 
     }
     if constexpr (kE4m3) {
       if (warp == 15) {
-        // -------------------------------------------------------- is the unit wide? A unit or two ahead
-        const int ps16 = p.page_shift - 4;
-        for (int u = u_begin; u < u_end; ++u) {
+        // -------------------------------------------------------- is the unit wide? A unit or two ahead, after the first
+        for (int u = u_begin + 1; u < u_end; ++u) {
           const PagedUnit un = p.units[u];
-          const int* pages = p.pages + un.page0;
           ScaleSpan keys, values;
-          constexpr int kAhead = 4;  // pieces of 16 rows of a lane on their way
-          for (int c0 = (un.key0 >> 4) + lane; c0 * 16 < un.key1; c0 += 32 * kAhead) {
-            uint4 k[kAhead], v[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-              const int c = c0 + 32 * i;
-              if (c * 16 < un.key1) {
-                const int row = ((pages[c >> ps16] * p.Hkv + un.head) << p.page_shift) + ((c & ((1 << ps16) - 1)) << 4);
-                k[i] = *reinterpret_cast<const uint4*>(p.pool.ks + row);
-                v[i] = *reinterpret_cast<const uint4*>(p.pool.vs + row);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-              const int rem = un.key1 - (c0 + 32 * i) * 16;
-              if (rem > 0) {
-                keys.take(k[i], rem);
-                values.take(v[i], rem);
-              }
-            }
-          }
-          const bool key_wide = keys.beyond(kKeySpan, kKeyTop), value_wide = values.beyond(kValueSpan, 255);
-          const int slot = (u - u_begin) & 1;
+          scan_scales(p, un, lane, 32, keys, values);
+          const bool wide = is_wide(keys.largest(), keys.smallest(), values.largest(), values.smallest());
+          const int n = u - u_begin - 1, slot = n & 1;
           if (lane == 0) {
-            mbar_wait(&wide_empty[slot], (((u - u_begin) >> 1) & 1) ^ 1u, wg);
-            wide_flag[slot] = key_wide || value_wide;
+            mbar_wait(&wide_empty[slot], ((n >> 1) & 1) ^ 1u, wg);
+            wide_flag[slot] = wide;
             mbar_arrive(&wide_full[slot]);
           }
           __syncwarp();
