@@ -144,7 +144,9 @@ mot_status mot_paged_query_workspace(mot_paged_batch_t bt, size_t* workspace_byt
  *        then k heads, then v heads
  *   q    device bf16 [T, Hq, 128]: RoPE_p(RMSNorm(q_h) * q_norm), one rounding
  * and into the pages, at each token's row, RoPE_p(RMSNorm(k_h) * k_norm) and
- * v_h. Statistics and rotation are f32; k goes to the pages with one rounding.
+ * v_h. Statistics and rotation are f32 (a head whose sum of squares passes f32, from
+ * magnitudes of about 2^60 on, comes out as zeros); k goes to the pages with one
+ * rounding.
  * The rest of the pool is left as it was. */
 mot_status mot_paged_append(mot_paged_t h, mot_paged_batch_t bt, const void* qkv, const mot_paged_pool* pool, void* q,
                             void* stream);

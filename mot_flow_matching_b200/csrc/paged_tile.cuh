@@ -20,9 +20,10 @@
 // tile's largest scale goes into the scores (keys), and into the weights
 // relative to the largest so far (values), as one factor per tile; queries are
 // made f16 in place, each row scaled by a power of two that its thread puts back.
-// Where a unit's scales lie too far apart for that (`kKeySpan`, `kValueSpan`; warp
-// 15 reads them a unit or two ahead), the operand tiles are bf16 instead, which
-// holds payload times scale, and the queries, as they are.
+// Where a unit's scales lie too far apart for that (`kKeySpan`, `kValueSpan`; warps
+// 8-11 read those of the first unit, warp 15 the others a unit or two ahead), the
+// operand tiles are bf16 instead, which holds payload times scale, and the queries,
+// as they are.
 // Scores of unseen keys become -infinity. Their values meet weights of zero, so in
 // tiles that not all rows of a unit see warps 8-11 take out what is not finite,
 // and rows that do see it get NaN in those dims at the end (bf16 pages go through
@@ -41,12 +42,12 @@
 // the kernel a query tile's chain S -> softmax -> P V -> next S takes about 3000:
 // 950 waiting for S, 170 to read it, 200 for the max, 1500 for exponentials and P
 // (1024 of the MUFU). Two query tiles overlap but do not hide it, and TMEM has no
-// room for a third. 2 x 4096 image tokens over 4496 keys (603 GFLOP): 554 us back
+// room for a third. 2 x 4096 image tokens over 4496 keys (603 GFLOP): 551 us back
 // to back (1.09 PFLOP/s). Prompt chunks of 129 to 512 tokens, bf16: 75 us. A mixed
-// e4m3 batch 256 us, 321 when every unit is wide; one chunk of 64 tokens over 64 e4m3
-// keys 14 us, over 4500 40 us. Of these the care for wide units, large scores and
-// values that are not finite costs 1% (image), 1% (chunks), 7%, 2 and 3 us; the scan of
-// a unit's scales alone 1.2 us a call. Spills, -Xptxas -v: 8 bytes stored (bf16), 148
+// e4m3 batch 248 us, 324 when every unit is wide; one chunk of 64 tokens over 64 e4m3
+// keys 14 us, over 4500 39 us. Of these the care for wide units, large scores and
+// values that are not finite costs up to 1% (image, chunks), 4%, 2.5 and 2.4 us; the scan
+// of a unit's scales alone 1.2 us a call. Spills, -Xptxas -v: 8 bytes stored (bf16), 236
 // (e4m3). Tried against the kernel of the time and slower: a quarter of the
 // exponentials by polynomial (image 564 against 555 us, a mixed e4m3 batch 289 against
 // 269), a second MMA warp (image 565 against 552), e4m3 conversion on eight warps with
