@@ -1,5 +1,6 @@
 """Calls of the paged prefix-KV cache (include/mot_paged.h) around the kernels:
 addresses that are no device memory of the current device, the `stream` argument, what a failed call leaves behind."""
+import gc
 from ctypes import byref, c_void_p
 
 import pytest
@@ -73,14 +74,17 @@ def test_a_workspace_is_kept_for_every_stream_that_uses_it(cuda_ready):
     q = torch.randn(1, 8, 128, device="cuda", dtype=torch.bfloat16)
     batch, side = paged.new_batch(), torch.cuda.Stream()
     batch.set(q_len, kv_len, table, n_pages)
-    paged.attend(batch, q, pool)
+    o = paged.attend(batch, q, pool)
     at, n = batch.workspace().data_ptr(), batch.workspace_bytes
+    gc.collect()  # handles of other tests
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(200_000_000)
-    paged.attend(batch, q, pool, stream=side)
+        torch.cuda._sleep(500_000_000)
+    paged.attend(batch, q, pool, o=o, stream=side)
     batch._ws = None  # as when the batch goes, but without the wait of its cudaFree
-    assert torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr() != at  # the side stream is not done with it
+    fresh = torch.empty(n, dtype=torch.uint8, device="cuda")
+    # not its memory while the side stream is at work (any cudaFree in this process waits for it: then nothing is shown)
+    assert fresh.data_ptr() != at or side.query()
     torch.cuda.synchronize()
 
 
