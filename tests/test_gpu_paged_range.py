@@ -270,12 +270,15 @@ def test_a_value_that_is_not_finite_costs_no_time(cuda_ready, kv):
             dense[1][:, :, -1, 0] = float("nan")
         paged, pool, table, batch = cached(16, hkv, 64, kv, [q_len] * n, [length] * n, *dense)
         attend(paged, pool, batch, q)
-        a, b = torch.cuda.Event(True), torch.cuda.Event(True)
-        a.record()
-        for _ in range(5):
-            o = paged.attend(batch, q, pool)
-        b.record()
-        torch.cuda.synchronize()
-        times.append(a.elapsed_time(b))
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            for _ in range(5):
+                o = paged.attend(batch, q, pool)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
         assert torch.isfinite(o.view(n, q_len, 16, 128)[:, :-1]).all()
     assert paged.device_status() == 0 and times[1] < 2 * times[0], times
